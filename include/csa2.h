@@ -355,6 +355,91 @@ int32_t csa2_fp4_quantize_bf16(const uint16_t* x, int64_t n_rows, int32_t D, int
                                uint8_t* scales, int64_t ld_scales, int64_t n_dst_rows,
                                int32_t* status, void* stream);
 
+/* ------------------------------------------------------------ grouped-query layers
+ * Layers that keep separate keys and values per head, beside the latent rows
+ * of the CSA2 layers: dense layers, and sliding-window layers with sink tokens
+ * (the pages name a sliding-window attention: "DeepSeek V4.1-Flash: 552B runs
+ * like 16B", Act 3).  Their cache is stored in the same FP4 format; the pages
+ * give its layout no form.
+ *
+ * The cache: Hkv key heads and Hkv value heads of D values per position, in
+ * four planes.  A code row holds the heads one after another, D/2 bytes each
+ * (row_bytes >= Hkv D/2, a multiple of 16); a scale row D/32 bytes each
+ * (row_bytes >= Hkv D/32, a multiple of D/32).  Paged or contiguous as every
+ * csa2_rows; a position at or past seq_rows of a contiguous plane whose
+ * seq_rows is not 0 is out of range (CSA2_ERR_INDEX_RANGE).  The planes may be
+ * the same memory (keys that are their own values).
+ */
+typedef struct csa2_kv_cache {
+  csa2_rows k_codes, k_scales, v_codes, v_scales;
+  int32_t Hkv, D;
+} csa2_kv_cache;
+
+/* csa2_kv_append_fp4: rotate the queries and keys of n tokens by their
+ * positions and store keys and values in the cache.
+ *   q, k, v     float rows of Hq, Hkv and Hkv heads of D values, token i at
+ *               i*ld_q, i*ld_k, i*ld_v (in values; multiples of 4, for the
+ *               bf16 call of 8; 16-byte aligned); q NULL with Hq = 0: no queries
+ *   seq_of_row  int32 [n] or NULL (token i belongs to sequence i)
+ *   row_pos     int32 [n]; a negative position marks a padding row, which
+ *               reads and writes nothing
+ *   cos_sin     float [n_pos][rot]: rot/2 cosines, then rot/2 sines, of each
+ *               position's angles (16-byte aligned); rot = 0: no rotation
+ *   rot         the first rot values of every query and key head turn, in pairs
+ *               (2i, 2i+1) if `interleaved`, else (i, i + rot/2):
+ *               a' = a cos - b sin, b' = b cos + a sin, in fp32
+ *   q_out       bf16 [n][Hq][D]; may be q itself in the bf16 call (ld_q = Hq D)
+ *   k_out, v_out  bf16 [n][Hkv][D] or NULL: the values as stored (code x scale)
+ * Keys and values are quantised as csa2_fp4_quantize does, from fp32; further,
+ * a block that holds a NaN is stored with the NaN scale 0x7F and zero codes,
+ * and infinities as +-6 x 448.  A token whose position or row is out of range
+ * is not stored at all (CSA2_ERR_INDEX_RANGE).  Two tokens of one call must
+ * not name the same position of a sequence: the row would hold a mix.
+ * Supported: D in {64, 128}; 1 <= Hkv <= 256; 0 <= Hq <= 1024; rot a multiple
+ * of 16 in [0, D]; n >= 0.
+ */
+int32_t csa2_kv_append_fp4(const float* q, const float* k, const float* v, int32_t n, int32_t Hq,
+                           int64_t ld_q, int64_t ld_k, int64_t ld_v, const int32_t* seq_of_row,
+                           const int32_t* row_pos, const float* cos_sin, int64_t n_pos, int32_t rot,
+                           int32_t interleaved, const csa2_kv_cache* cache, uint16_t* q_out, uint16_t* k_out,
+                           uint16_t* v_out, int32_t* status, void* stream);
+/* csa2_kv_append_fp4_bf16: the same for bf16 rows. */
+int32_t csa2_kv_append_fp4_bf16(const uint16_t* q, const uint16_t* k, const uint16_t* v, int32_t n, int32_t Hq,
+                                int64_t ld_q, int64_t ld_k, int64_t ld_v, const int32_t* seq_of_row,
+                                const int32_t* row_pos, const float* cos_sin, int64_t n_pos, int32_t rot,
+                                int32_t interleaved, const csa2_kv_cache* cache, uint16_t* q_out,
+                                uint16_t* k_out, uint16_t* v_out, int32_t* status, void* stream);
+
+/* csa2_gqa_attn_fp4: softmax attention of each query over the cached rows it
+ * sees.  Query head h reads KV head h / (Hq / Hkv).
+ *   q            bf16 [nq][Hq][D]
+ *   query_pos    int32 [nq]; a query sees rows 0..query_pos[i]; a negative
+ *                position sees none: its output is 0 and its lse -inf
+ *   softmax_scale  host; <= 0 means 1/sqrt(D)
+ *   group_queries  nonzero: consecutive queries of one sequence share the rows
+ *                they read (a prefill chunk, a speculative block); zero: every
+ *                query reads alone (a decode batch).  The results are the same
+ *                up to rounding, whatever the sequences and positions.
+ *   out          bf16 [nq][Hq][D];  lse float [nq][Hq] or NULL, as
+ *                csa2_sparse_attn_fp4 (parts combine with csa2_attn_combine)
+ * Accumulation is fp32.  No value of a row that a query does not see reaches
+ * its output, whatever bytes the row holds.  Supported: D in {64, 128}; Hq a
+ * multiple of Hkv; 1 <= Hkv <= 256; Hq <= 1024; 1 <= nq <= 16384.
+ */
+int32_t csa2_gqa_attn_fp4(const uint16_t* q, const csa2_kv_cache* cache, const int32_t* seq_of_query,
+                          const int32_t* query_pos, int32_t nq, int32_t Hq, float softmax_scale,
+                          int32_t group_queries, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                          int32_t* status, void* stream);
+/* csa2_gqa_window_attn_fp4: the same with a sliding window and sinks: a query
+ * at position p sees the rows in [p - window + 1, p] and those of the first
+ * n_sink positions that are not past p.  window >= 1, n_sink >= 0. */
+int32_t csa2_gqa_window_attn_fp4(const uint16_t* q, const csa2_kv_cache* cache, const int32_t* seq_of_query,
+                                 const int32_t* query_pos, int32_t nq, int32_t Hq, int32_t window,
+                                 int32_t n_sink, float softmax_scale, int32_t group_queries, uint16_t* out,
+                                 float* lse, void* ws, size_t ws_bytes, int32_t* status, void* stream);
+/* Workspace of both calls (0: unsupported shape). */
+size_t csa2_gqa_attn_workspace(int32_t nq, int32_t Hq, int32_t Hkv, int32_t D);
+
 /* ------------------------------------------------------------ helpers */
 const char* csa2_status_string(int32_t status);  /* static string, never NULL */
 int32_t csa2_version(void);                       /* major*10000 + minor*100 + patch */

@@ -6,8 +6,9 @@ workspaces, the status word) and the stream.  There is no fallback: if the
 library cannot be loaded, every call raises.
 
 The functions keep the C names: csa2_index_full, csa2_topk_pool,
-csa2_reindex, csa2_sparse_attn_fp4, csa2_layer_plan and csa2_fp4_quantize.
-Each takes torch tensors.  It allocates the workspace the library asks for
+csa2_reindex, csa2_sparse_attn_fp4, csa2_layer_plan, csa2_fp4_quantize, and for
+grouped-query layers csa2_kv_append_fp4, csa2_gqa_attn_fp4 and
+csa2_gqa_window_attn_fp4.  Each takes torch tensors.  It allocates the workspace the library asks for
 (unless one is passed) and raises Csa2Error on a non-zero return.  Errors
 found on the device land in the int32 ``status`` tensor; check_status() reads
 it, which synchronises.
@@ -48,6 +49,11 @@ class csa2_layer(ctypes.Structure):
                 ("local_kv", csa2_rows)]
 
 
+class csa2_kv_cache(ctypes.Structure):
+    _fields_ = [("k_codes", csa2_rows), ("k_scales", csa2_rows), ("v_codes", csa2_rows), ("v_scales", csa2_rows),
+                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32)]
+
+
 class csa2_plan_shape(ctypes.Structure):
     _fields_ = [("nq", ctypes.c_int32), ("H", ctypes.c_int32), ("D_idx", ctypes.c_int32),
                 ("Hq", ctypes.c_int32), ("D", ctypes.c_int32), ("P", ctypes.c_int32),
@@ -58,6 +64,8 @@ class csa2_plan_shape(ctypes.Structure):
 
 _P, _I32, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _RP = ctypes.POINTER(csa2_rows)
+_CP = ctypes.POINTER(csa2_kv_cache)
+_APPEND = (_I32, [_P, _P, _P, _I32, _I32, _I64, _I64, _I64, _P, _P, _P, _I64, _I32, _I32, _CP, _P, _P, _P, _P, _P])
 _SIGS = {
     "csa2_index_full": (_I32, [_P, _P, _RP, _P, _P, _I32, _I32, _I32, _I32, _P, _I64, _I32, _P, _P, _I32,
                                _P, _P, _P, _SZ, _P, _P]),
@@ -79,6 +87,11 @@ _SIGS = {
     "csa2_attn_combine": (_I32, [_P, _P, _I32, _I32, _I32, _I32, _P, _P, _P, _P]),
     "csa2_fp4_quantize": (_I32, [_P, _I64, _I32, _I64, _P, _P, _I64, _P, _I64, _I64, _P, _P]),
     "csa2_fp4_quantize_bf16": (_I32, [_P, _I64, _I32, _I64, _P, _P, _I64, _P, _I64, _I64, _P, _P]),
+    "csa2_kv_append_fp4": _APPEND,
+    "csa2_kv_append_fp4_bf16": _APPEND,
+    "csa2_gqa_attn_fp4": (_I32, [_P, _CP, _P, _P, _I32, _I32, _F, _I32, _P, _P, _P, _SZ, _P, _P]),
+    "csa2_gqa_window_attn_fp4": (_I32, [_P, _CP, _P, _P, _I32, _I32, _I32, _I32, _F, _I32, _P, _P, _P, _SZ, _P, _P]),
+    "csa2_gqa_attn_workspace": (_SZ, [_I32, _I32, _I32, _I32]),
     "csa2_status_string": (ctypes.c_char_p, [_I32]),
     "csa2_version": (_I32, []),
     "csa2_selftest_wait": (_I32, [_I32, ctypes.c_uint64, _P, _P, _P]),
@@ -382,3 +395,181 @@ def csa2_layer_plan(modes, layers: list[Layer], **kw) -> LayerPlan:
     plan = LayerPlan(modes, layers, **kw)
     plan.run()
     return plan
+
+
+# ----------------------------------------------------------------- grouped-query layers
+class KVCache:
+    """The FP4 cache of a grouped-query layer: K and V heads of D values per
+    position in four planes (see csa2_kv_cache).  The C struct is made once, so
+    the planes and the page table are the ones given here; their contents may
+    change from call to call."""
+
+    def __init__(self, Hkv: int, D: int, k_codes: Rows, k_scales: Rows, v_codes: Rows, v_scales: Rows):
+        self.Hkv, self.D = Hkv, D
+        self.keep = (k_codes, k_scales, v_codes, v_scales)
+        self.device = k_codes.data.device
+        c = csa2_kv_cache()
+        for name, r in zip(("k_codes", "k_scales", "v_codes", "v_scales"), self.keep):
+            if r.data.element_size() != 1:
+                raise ValueError(f"{name} must hold bytes")
+            if r.data.device != self.device or (r.page_table is not None and r.page_table.device != self.device):
+                raise ValueError("the planes and page tables of a cache must be on one device")
+            setattr(c, name, r.c())
+        c.Hkv, c.D = Hkv, D
+        self.c = c
+
+
+class _Call:
+    """A marshalled C call: run() is one call into the library (and can be
+    captured in a CUDA graph).  It keeps every tensor it was made with."""
+
+    scratch: tuple = ()      # tensors made here: held back from reuse while another stream works with them
+
+    def _make(self, name, device, args, keep, status):
+        if device.type != "cuda":
+            raise ValueError(f"{name}: the cache must be on a CUDA device")
+        for n, t in keep.items():
+            if t is not None and t.device != device:
+                raise ValueError(f"{name}: {n} is on {t.device}, the cache on {device}")
+        self.name, self.device, self.keep = name, device, keep
+        if status is None:
+            status = new_status(device)
+            self.scratch += (status,)
+        self.status = status
+        _dev(self.status, torch.int32, "status")
+        if self.status.device != device:
+            raise ValueError(f"{name}: status is on {self.status.device}, the cache on {device}")
+        self.fn = getattr(lib(), name)
+        # converted once: ctypes then passes the same objects every time
+        self.args = tuple(t(x) if t in (_P, _I32, _I64, _SZ, _F) else x
+                          for t, x in zip(self.fn.argtypes, (*args, _ptr(self.status))))
+
+    def run(self, stream=None) -> None:
+        if torch.cuda.current_device() != self.device.index:
+            raise ValueError(f"{self.name}: the cache is on {self.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        if stream is not None:
+            for t in self.scratch:
+                t.record_stream(stream)
+        _check(self.fn(*self.args, _stream(stream)), self.name)
+
+
+def _heads(t, n_heads, D, dtype, n, name) -> int:
+    """The row stride in values of t [n][n_heads][D], whose heads lie one after another."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != (n, n_heads, D):
+        raise ValueError(f"{name} must have shape {(n, n_heads, D)}, got {tuple(t.shape)}")
+    if t.stride(2) != 1 or (n_heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a row must lie one after another")
+    return t.stride(0) if n > 1 else max(t.stride(0), n_heads * D)
+
+
+def _index(t, n, name) -> None:
+    if t is not None:
+        _dev(t, torch.int32, name)
+        if t.numel() != n:
+            raise ValueError(f"{name} must hold {n} values, got {t.numel()}")
+
+
+def _whole(t, shape, dtype, name) -> None:
+    if t is not None:
+        _dev(t, dtype, name)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+class KVAppend(_Call):
+    """A marshalled csa2_kv_append_fp4 call; see csa2_kv_append_fp4."""
+
+    def __init__(self, cache: KVCache, k, v, row_pos, *, seq_of_row=None, cos_sin=None, interleaved: bool = False,
+                 q=None, q_out=None, k_out=None, v_out=None, status=None):
+        Hkv, D, n, dt = cache.Hkv, cache.D, k.shape[0], k.dtype
+        if dt not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"k must be float32 or bfloat16, got {dt}")
+        ld_k, ld_v = _heads(k, Hkv, D, dt, n, "k"), _heads(v, Hkv, D, dt, n, "v")
+        Hq = ld_q = 0
+        if q is not None:
+            Hq = q.shape[1]
+            ld_q = _heads(q, Hq, D, dt, n, "q")
+            if q_out is None:
+                raise ValueError("q needs q_out")
+        _index(row_pos, n, "row_pos")
+        _index(seq_of_row, n, "seq_of_row")
+        _whole(q_out, (n, Hq, D), torch.bfloat16, "q_out")
+        _whole(k_out, (n, Hkv, D), torch.bfloat16, "k_out")
+        _whole(v_out, (n, Hkv, D), torch.bfloat16, "v_out")
+        n_pos = rot = 0
+        if cos_sin is not None:
+            _dev(cos_sin, torch.float32, "cos_sin")
+            n_pos, rot = cos_sin.shape
+        self.cache = cache
+        name = "csa2_kv_append_fp4_bf16" if dt == torch.bfloat16 else "csa2_kv_append_fp4"
+        self._make(name, cache.device, (_ptr(q), _ptr(k), _ptr(v), n, Hq, ld_q, ld_k, ld_v, _ptr(seq_of_row),
+                                        _ptr(row_pos), _ptr(cos_sin), n_pos, rot, int(interleaved),
+                                        ctypes.byref(cache.c), _ptr(q_out), _ptr(k_out), _ptr(v_out)),
+                   dict(q=q, k=k, v=v, seq_of_row=seq_of_row, row_pos=row_pos, cos_sin=cos_sin, q_out=q_out,
+                        k_out=k_out, v_out=v_out), status)
+
+
+class GqaAttn(_Call):
+    """A marshalled csa2_gqa_attn_fp4 (or, with ``window``,
+    csa2_gqa_window_attn_fp4) call with a workspace of its own."""
+
+    def __init__(self, cache: KVCache, q, query_pos, out, *, seq_of_query=None, window: int = 0, n_sink: int = 0,
+                 softmax_scale: float = 0.0, lse=None, group_queries: bool = False, status=None, ws=None):
+        nq, Hq, D = q.shape
+        _dev(q, torch.bfloat16, "q")
+        if D != cache.D:
+            raise ValueError(f"q has heads of {D} values, the cache of {cache.D}")
+        _whole(out, (nq, Hq, D), torch.bfloat16, "out")
+        _whole(lse, (nq, Hq), torch.float32, "lse")
+        _index(query_pos, nq, "query_pos")
+        _index(seq_of_query, nq, "seq_of_query")
+        if window < 0 or n_sink < 0 or (n_sink > 0 and window == 0):
+            raise ValueError("window and n_sink must not be negative, and sinks need a window")
+        need = lib().csa2_gqa_attn_workspace(nq, Hq, cache.Hkv, D)
+        if need == 0:
+            raise Csa2Error(2, "csa2_gqa_attn_workspace")
+        if ws is None:
+            ws = _workspace(need, cache.device)
+            self.scratch = (ws,)
+        _dev(ws, torch.uint8, "ws")
+        self.cache = cache
+        name = "csa2_gqa_window_attn_fp4" if window else "csa2_gqa_attn_fp4"
+        self._make(name, cache.device, (_ptr(q), ctypes.byref(cache.c), _ptr(seq_of_query), _ptr(query_pos), nq, Hq,
+                                        *((window, n_sink) if window else ()), softmax_scale, int(group_queries),
+                                        _ptr(out), _ptr(lse), _ptr(ws), ws.numel()),
+                   dict(q=q, seq_of_query=seq_of_query, query_pos=query_pos, out=out, lse=lse, ws=ws), status)
+
+
+def csa2_kv_append_fp4(cache: KVCache, k, v, row_pos, *, stream=None, **kw) -> torch.Tensor:
+    """Rotates and stores the keys k and values v [n][Hkv][D] (float32 or
+    bfloat16) of n tokens at positions row_pos (negative: padding) in the
+    cache.  cos_sin float32 [n_pos][rot] holds each position's cosines, then
+    sines; q [n][Hq][D] is rotated into q_out (bfloat16); k_out and v_out take
+    the values as stored.  Returns the status tensor."""
+    call = KVAppend(cache, k, v, row_pos, **kw)
+    call.run(stream)
+    return call.status
+
+
+def csa2_gqa_attn_fp4(cache: KVCache, q, query_pos, out, *, stream=None, **kw) -> torch.Tensor:
+    """Attention of q bf16 [nq][Hq][D] over every cached row up to each
+    query's position.  ``group_queries`` lets consecutive queries of a sequence
+    share the rows they read.  Returns the status tensor."""
+    if kw.get("window") or kw.get("n_sink"):
+        raise ValueError("csa2_gqa_attn_fp4 sees every row; use csa2_gqa_window_attn_fp4")
+    call = GqaAttn(cache, q, query_pos, out, **kw)
+    call.run(stream)
+    return call.status
+
+
+def csa2_gqa_window_attn_fp4(cache: KVCache, q, query_pos, out, window: int, n_sink: int = 0, *, stream=None,
+                             **kw) -> torch.Tensor:
+    """csa2_gqa_attn_fp4 over the last ``window`` rows and the first ``n_sink``."""
+    if window < 1:
+        raise ValueError("window must be at least 1")
+    call = GqaAttn(cache, q, query_pos, out, window=window, n_sink=n_sink, **kw)
+    call.run(stream)
+    return call.status

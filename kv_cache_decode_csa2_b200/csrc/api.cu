@@ -299,6 +299,99 @@ int32_t csa2_sparse_attn_fp4_local(const uint16_t* q, const csa2_rows* codes, co
                   softmax_scale, out, lse, ws, ws_bytes, status, stream);
 }
 
+// ------------------------------------------------------------------ grouped-query layers
+static bool kv_shape_ok(int32_t Hq, int32_t Hkv, int32_t D) {
+  return (D == 64 || D == 128) && Hkv >= 1 && Hkv <= 256 && Hq >= 0 && Hq <= 1024;
+}
+static bool kv_cache_ok(const csa2_kv_cache* c) {
+  return rows_ok(&c->k_codes, (int64_t)c->Hkv * c->D / 2, 16) && rows_ok(&c->v_codes, (int64_t)c->Hkv * c->D / 2, 16) &&
+         rows_ok(&c->k_scales, (int64_t)c->Hkv * c->D / 32, c->D / 32) &&
+         rows_ok(&c->v_scales, (int64_t)c->Hkv * c->D / 32, c->D / 32);
+}
+
+static int32_t run_kv_append(const void* q, const void* k, const void* v, bool f32, int32_t n, int32_t Hq,
+                             int64_t ld_q, int64_t ld_k, int64_t ld_v, const int32_t* seq_of_row,
+                             const int32_t* row_pos, const float* cos_sin, int64_t n_pos, int32_t rot,
+                             int32_t interleaved, const csa2_kv_cache* cache, uint16_t* q_out, uint16_t* k_out,
+                             uint16_t* v_out, int32_t* status, void* stream) {
+  const int64_t align = f32 ? 4 : 8;
+  if (!cache || !status || n < 0 || (n > 0 && (!k || !v || !row_pos))) return CSA2_ERR_INVALID_ARG;
+  if (!kv_shape_ok(Hq, cache->Hkv, cache->D)) return CSA2_ERR_UNSUPPORTED;
+  if (rot < 0 || rot > cache->D || rot % 16) return CSA2_ERR_UNSUPPORTED;
+  if (!kv_cache_ok(cache)) return CSA2_ERR_INVALID_ARG;
+  if (n == 0) return CSA2_OK;
+  const int64_t kv = (int64_t)cache->Hkv * cache->D;
+  if (ld_k < kv || ld_v < kv || ld_k % align || ld_v % align || !aligned(k, 16) || !aligned(v, 16))
+    return CSA2_ERR_INVALID_ARG;
+  if (Hq > 0 ? !q || !q_out || ld_q < (int64_t)Hq * cache->D || ld_q % align || !aligned(q, 16) || !aligned(q_out, 16)
+             : q != nullptr)
+    return CSA2_ERR_INVALID_ARG;
+  if (rot > 0 && (!cos_sin || !aligned(cos_sin, 16) || n_pos < 1)) return CSA2_ERR_INVALID_ARG;
+  if (!aligned(k_out, 16) || !aligned(v_out, 16)) return CSA2_ERR_INVALID_ARG;
+  return cuda_status(launch_kv_append(q, k, v, f32, n, Hq, ld_q, ld_k, ld_v, seq_of_row, row_pos, cos_sin, n_pos,
+                                      rot, interleaved != 0, *cache, q_out, k_out, v_out, status,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+int32_t csa2_kv_append_fp4(const float* q, const float* k, const float* v, int32_t n, int32_t Hq, int64_t ld_q,
+                           int64_t ld_k, int64_t ld_v, const int32_t* seq_of_row, const int32_t* row_pos,
+                           const float* cos_sin, int64_t n_pos, int32_t rot, int32_t interleaved,
+                           const csa2_kv_cache* cache, uint16_t* q_out, uint16_t* k_out, uint16_t* v_out,
+                           int32_t* status, void* stream) {
+  CSA2_API_RANGE("csa2_kv_append_fp4");
+  return run_kv_append(q, k, v, true, n, Hq, ld_q, ld_k, ld_v, seq_of_row, row_pos, cos_sin, n_pos, rot, interleaved,
+                       cache, q_out, k_out, v_out, status, stream);
+}
+
+int32_t csa2_kv_append_fp4_bf16(const uint16_t* q, const uint16_t* k, const uint16_t* v, int32_t n, int32_t Hq,
+                                int64_t ld_q, int64_t ld_k, int64_t ld_v, const int32_t* seq_of_row,
+                                const int32_t* row_pos, const float* cos_sin, int64_t n_pos, int32_t rot,
+                                int32_t interleaved, const csa2_kv_cache* cache, uint16_t* q_out, uint16_t* k_out,
+                                uint16_t* v_out, int32_t* status, void* stream) {
+  CSA2_API_RANGE("csa2_kv_append_fp4_bf16");
+  return run_kv_append(q, k, v, false, n, Hq, ld_q, ld_k, ld_v, seq_of_row, row_pos, cos_sin, n_pos, rot, interleaved,
+                       cache, q_out, k_out, v_out, status, stream);
+}
+
+size_t csa2_gqa_attn_workspace(int32_t nq, int32_t Hq, int32_t Hkv, int32_t D) {
+  if (nq < 1 || nq > 16384 || !kv_shape_ok(Hq, Hkv, D) || Hq < 1 || Hq % Hkv) return 0;
+  return gqa_scratch_bytes(nq, Hq, Hkv, D);
+}
+
+static int32_t run_gqa_attn(const uint16_t* q, const csa2_kv_cache* cache, const int32_t* seq_of_query,
+                            const int32_t* query_pos, int32_t nq, int32_t Hq, int32_t window, int32_t n_sink,
+                            float softmax_scale, int32_t group_queries, uint16_t* out, float* lse, void* ws,
+                            size_t ws_bytes, int32_t* status, void* stream) {
+  if (!q || !cache || !query_pos || !out || !status || !aligned(q, 16) || !aligned(out, 16) || nq < 1)
+    return CSA2_ERR_INVALID_ARG;
+  const size_t need = csa2_gqa_attn_workspace(nq, Hq, cache->Hkv, cache->D);
+  if (need == 0) return CSA2_ERR_UNSUPPORTED;
+  if (!kv_cache_ok(cache)) return CSA2_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, 256) || ws_bytes < need) return CSA2_ERR_WORKSPACE;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)cache->D);
+  return cuda_status(launch_gqa_attn(q, *cache, seq_of_query, query_pos, nq, Hq, window, n_sink, scale,
+                                     group_queries != 0, out, lse, ws, status, static_cast<cudaStream_t>(stream)));
+}
+
+int32_t csa2_gqa_attn_fp4(const uint16_t* q, const csa2_kv_cache* cache, const int32_t* seq_of_query,
+                          const int32_t* query_pos, int32_t nq, int32_t Hq, float softmax_scale,
+                          int32_t group_queries, uint16_t* out, float* lse, void* ws, size_t ws_bytes,
+                          int32_t* status, void* stream) {
+  CSA2_API_RANGE("csa2_gqa_attn_fp4");
+  return run_gqa_attn(q, cache, seq_of_query, query_pos, nq, Hq, 0, 0, softmax_scale, group_queries, out, lse, ws,
+                      ws_bytes, status, stream);
+}
+
+int32_t csa2_gqa_window_attn_fp4(const uint16_t* q, const csa2_kv_cache* cache, const int32_t* seq_of_query,
+                                 const int32_t* query_pos, int32_t nq, int32_t Hq, int32_t window, int32_t n_sink,
+                                 float softmax_scale, int32_t group_queries, uint16_t* out, float* lse, void* ws,
+                                 size_t ws_bytes, int32_t* status, void* stream) {
+  CSA2_API_RANGE("csa2_gqa_window_attn_fp4");
+  if (window < 1 || n_sink < 0) return CSA2_ERR_INVALID_ARG;
+  return run_gqa_attn(q, cache, seq_of_query, query_pos, nq, Hq, window, n_sink, softmax_scale, group_queries, out,
+                      lse, ws, ws_bytes, status, stream);
+}
+
 // ------------------------------------------------------------------ layer plan
 namespace {
 

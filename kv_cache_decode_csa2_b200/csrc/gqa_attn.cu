@@ -1,0 +1,627 @@
+// Grouped-query attention over the FP4 cache, a few query heads per KV head:
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - m)
+// over the rows j that the query sees (all up to its own position, or a
+// window and the first rows), in one pass with a running maximum m.
+//
+// Bound by HBM: a row is D (1/2 + 1/32) bytes each of K and V per KV head,
+// read once for all the query heads that share it.  A warp owns one KV head
+// (up to 8 NT of its query heads) and walks 16-row tiles:
+//   S^T [16 rows][heads] = K Q^T,   O^T [D][heads] += V^T P^T
+// on m16n8k16 MMAs whose M side is the cache, so 8 heads fill an MMA and no
+// row of it is padding.  Codes go from global memory to the MMA operand in
+// registers: the contraction order is free, so lane t of a row's quad owns a
+// contiguous quarter of the head dimension (one 16-byte load, one scale), and
+// of V^T lane g owns a contiguous eighth of it in four rows, two of which are
+// interleaved nibble by nibble so that one E2M1 conversion makes the operand
+// pair.  code x scale is exact in f16 (at most 6 significant bits, 2^-10 to
+// 2688).  A query row is scaled by a power of two into f16, which keeps all
+// of bf16's 8 bits for values down to 2^-28 of the row's largest.
+//
+// The maximum is lazy: m moves only when a logit exceeds it by 5 (log2), and
+// weights are 2^(s - m + 10) <= 2^15.  A row's largest is then at least 2^10,
+// so in f16 a weight keeps 11 bits down to 2^-24 of the largest and vanishes
+// only below 2^-35: a million rows of small weights beside one large sink
+// still count.  Sums are fp32 of the unrounded weights.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fp4_device.cuh"
+#include "gqa_attn.cuh"
+
+namespace csa2 {
+
+namespace {
+
+constexpr int kGqaThreads = 256;
+constexpr int kGqaWarps = kGqaThreads / 32;
+constexpr float kLazy = 5.f;          // how far a logit may exceed the maximum in use (log2)
+constexpr float kOffset = 10.f;       // weights are 2^(s - m + kOffset)
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Transposes an 8 x 8 matrix of 16-bit values held as two per lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// One 16-row tile of a KV head as a lane holds it: codes of rows g and g + 8
+// of K, of rows 2t, 2t + 1, 2t + 8, 2t + 9 of V, and their scales.
+template <int D>
+struct GqaTile {
+  uint32_t k[2][D / 32];
+  uint32_t v[4][D / 64];
+  uint32_t ks, vs;            // scale bytes: of K in bytes 0 and 1, of V in bytes 0 to 3
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  } else if constexpr (N == 2) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+  }
+}
+
+// First physical row of the tile at position p0 in each plane; false (and the
+// error recorded) when the rows up to `last` are not all in the plane.
+__device__ __forceinline__ bool tile_rows(const GqaArgs& a, int32_t seq, int32_t p0, int32_t last, int64_t (&r)[4]) {
+  const int32_t n = min(15, last - p0);
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i > 0 && a.one_map) {
+      r[i] = r[0];
+      continue;
+    }
+    const RowMap& m = a.map[i];
+    r[i] = seq < 0 || (!m.page_table && m.seq_rows > 0 && p0 + n >= m.seq_rows) ? -1 : map_row(m, seq, p0);
+    ok = ok && r[i] >= 0 && r[i] + n < m.n_rows;
+  }
+  return ok;
+}
+
+template <int D>
+__device__ __forceinline__ void load_tile(const GqaArgs& a, GqaTile<D>& x, const int64_t (&r)[4], int32_t p0,
+                                          int32_t pos, int head, int g, int t) {
+  x.ks = x.vs = 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int m = g + 8 * i;
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) x.k[i][w] = 0;
+    if (sees(p0 + m, pos, a.window, a.n_sink)) {
+      load_words(a.base[0] + (r[0] + m) * a.rb[0] + head * (D / 2) + t * (D / 8), x.k[i]);
+      x.ks |= (uint32_t)__ldg(a.base[1] + (r[1] + m) * a.rb[1] + head * (D / 32) + t * (D / 4) / 32) << (8 * i);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = 2 * t + (i & 1) + 8 * (i >> 1);
+#pragma unroll
+    for (int w = 0; w < D / 64; ++w) x.v[i][w] = 0;
+    if (sees(p0 + m, pos, a.window, a.n_sink)) {
+      load_words(a.base[2] + (r[2] + m) * a.rb[2] + head * (D / 2) + g * (D / 16), x.v[i]);
+      x.vs |= (uint32_t)__ldg(a.base[3] + (r[3] + m) * a.rb[3] + head * (D / 32) + g * (D / 8) / 32) << (8 * i);
+    }
+  }
+}
+
+// Running state of a warp: NT runs of 8 heads.  A lane holds heads 2t and
+// 2t + 1 of each run.
+template <int D, int NT>
+struct GqaState {
+  float o[NT][D / 16][4];     // O^T: dims g D/8 + 2j (+ 1), heads 2t and 2t + 1
+  float mo[NT][2];            // maximum in use minus kOffset, log2 units (-inf: no row yet)
+  float l[NT][2];             // this lane's part of the sum of weights
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void tile_step(const GqaArgs& a, GqaState<D, NT>& st, const GqaTile<D>& x,
+                                          const uint32_t (&qf)[NT][D / 16][2], const float (&qs)[NT][2], int32_t p0,
+                                          int32_t pos, int g) {
+  float s[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+  const uint32_t sk0 = e4m3x2_to_f16x2(__byte_perm(x.ks, 0, 0x0000)), sk1 = e4m3x2_to_f16x2(__byte_perm(x.ks, 0, 0x1111));
+#pragma unroll
+  for (int k = 0; k < D / 16; ++k) {
+    const uint32_t w0 = x.k[0][k / 2] >> (16 * (k & 1)), w1 = x.k[1][k / 2] >> (16 * (k & 1));
+    const uint32_t af[4] = {mul_f16x2(e2m1x2_to_f16x2(w0 & 0xFFu), sk0), mul_f16x2(e2m1x2_to_f16x2(w1 & 0xFFu), sk1),
+                            mul_f16x2(e2m1x2_to_f16x2((w0 >> 8) & 0xFFu), sk0),
+                            mul_f16x2(e2m1x2_to_f16x2((w1 >> 8) & 0xFFu), sk1)};
+#pragma unroll
+    for (int n = 0; n < NT; ++n) mma_f16(s[n], af, qf[n][k][0], qf[n][k][1]);
+  }
+  const bool see0 = sees(p0 + g, pos, a.window, a.n_sink), see1 = sees(p0 + g + 8, pos, a.window, a.n_sink);
+  bool more = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      s[n][e] = see0 ? s[n][e] * qs[n][e] : -INFINITY;
+      s[n][2 + e] = see1 ? s[n][2 + e] * qs[n][e] : -INFINITY;
+      more |= fmaxf(s[n][e], s[n][2 + e]) > st.mo[n][e] + (kOffset + kLazy);
+    }
+  if (__any_sync(0xffffffffu, more)) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float f[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float m = fmaxf(s[n][e], s[n][2 + e]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float mo = fmaxf(st.mo[n][e], m - kOffset);
+        f[e] = st.mo[n][e] == -INFINITY ? 0.f : ex2(st.mo[n][e] - mo);
+        st.mo[n][e] = mo;
+        st.l[n][e] *= f[e];
+      }
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st.o[n][j][i] *= f[i & 1];
+    }
+  }
+  uint32_t pf[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = ex2(s[n][i] - st.mo[n][i & 1]);
+    st.l[n][0] += p[0] + p[2];
+    st.l[n][1] += p[1] + p[3];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __half2 h = __floats2half2_rn(p[2 * i], p[2 * i + 1]);
+      pf[n][i] = transpose8x8(*reinterpret_cast<const uint32_t*>(&h));
+    }
+  }
+  const uint32_t sv0 = e4m3x2_to_f16x2(x.vs), sv1 = e4m3x2_to_f16x2(x.vs >> 16);
+#pragma unroll
+  for (int w = 0; w < D / 64; ++w) {
+    constexpr uint32_t kLow = 0x0F0F0F0Fu;
+    const uint32_t lo01 = (x.v[0][w] & kLow) | ((x.v[1][w] & kLow) << 4);
+    const uint32_t hi01 = ((x.v[0][w] >> 4) & kLow) | (x.v[1][w] & ~kLow);
+    const uint32_t lo23 = (x.v[2][w] & kLow) | ((x.v[3][w] & kLow) << 4);
+    const uint32_t hi23 = ((x.v[2][w] >> 4) & kLow) | (x.v[3][w] & ~kLow);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const uint32_t af[4] = {mul_f16x2(e2m1x2_to_f16x2((lo01 >> (8 * b)) & 0xFFu), sv0),
+                              mul_f16x2(e2m1x2_to_f16x2((hi01 >> (8 * b)) & 0xFFu), sv0),
+                              mul_f16x2(e2m1x2_to_f16x2((lo23 >> (8 * b)) & 0xFFu), sv1),
+                              mul_f16x2(e2m1x2_to_f16x2((hi23 >> (8 * b)) & 0xFFu), sv1)};
+#pragma unroll
+      for (int n = 0; n < NT; ++n) mma_f16(st.o[n][4 * w + b], af, pf[n][0], pf[n][1]);
+    }
+  }
+}
+
+// The query heads of a run as MMA operands, and their logit scales (log2
+// units) for the heads a lane holds.  Head n 8 + g, dims t D/4 + 4k + {0..3}.
+template <int D, int NT>
+__device__ __forceinline__ void load_query(const GqaArgs& a, const uint16_t* q, int heads, int g, int t,
+                                           uint32_t (&qf)[NT][D / 16][2], float (&qs)[NT][2]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int h = n * 8 + g;
+    uint32_t w[D / 8];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 u = h < heads ? __ldg(reinterpret_cast<const uint4*>(q + (int64_t)h * D + t * (D / 4)) + i)
+                                : make_uint4(0, 0, 0, 0);
+      w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+    }
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // the largest magnitude into [2^14, 2^15); rows below 2^-107 are scaled as that
+    const int e = max((int)(top >> 7), 20);
+    const float up = __uint_as_float((uint32_t)(268 - e) << 23);             // 2^(141 - e)
+    float down = __uint_as_float((uint32_t)max(e - 14, 1) << 23) * a.scale_log2;   // 2^(e - 141)
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const __half2 hh = __floats2half2_rn(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
+      qf[n][i / 2][i & 1] = *reinterpret_cast<const uint32_t*>(&hh);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) qs[n][x] = __shfl_sync(0xffffffffu, down, (2 * t + x) * 4);
+  }
+}
+
+// Sum over the block of one value per thread, and the sum of the threads
+// before this one.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sh, int64_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t n = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += n;
+  }
+  if (lane == 31) sh[warp] = s;
+  __syncthreads();
+  int64_t before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kGqaWarps; ++i) {
+    if (i < warp) before += sh[i];
+    all += sh[i];
+  }
+  *total = all;
+  return before + s - v;
+}
+
+template <int D>
+__device__ __forceinline__ void store_bf16(uint16_t* dst, const float* v, float w) {   // D/8 values
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    uint32_t p[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * i + 2 * j] * w, v[8 * i + 2 * j + 1] * w);
+      p[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    reinterpret_cast<uint4*>(dst)[i] = make_uint4(p[0], p[1], p[2], p[3]);
+  }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel(const __grid_constant__ GqaArgs a) {
+  extern __shared__ __align__(16) float merge_s[];     // [warps][8 NT][D + 2] when several warps share a head
+  __shared__ int64_t scan_s[kGqaWarps];
+  __shared__ int32_t item_s;
+  __shared__ int64_t item_start_s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  pdl_trigger();
+
+  // ---- where this CTA's run of units starts
+  int64_t total;
+  {
+    const int per = (a.nq + kGqaThreads - 1) / kGqaThreads;
+    const int i0 = min(tid * per, a.nq), i1 = min(i0 + per, a.nq);
+    int64_t n = 0;
+    for (int i = i0; i < i1; ++i) n += unit_range(__ldg(a.query_pos + i), a.window, a.n_sink).count;
+    int64_t start = block_scan(n, scan_s, &total);
+    const int64_t all = total * a.groups, run = (all + a.n_cta - 1) / a.n_cta;
+    const int64_t u = (int64_t)blockIdx.x * run;
+    if (blockIdx.x == 0 || (start * a.groups <= u && u < (start + n) * a.groups)) {
+      for (int i = i0; i < i1; ++i) {
+        const int64_t c = unit_range(__ldg(a.query_pos + i), a.window, a.n_sink).count;
+        if (blockIdx.x == 0) a.starts[i] = start;
+        if (start * a.groups <= u && u < (start + c) * a.groups) {
+          item_s = i;
+          item_start_s = start;
+        }
+        start += c;
+      }
+    }
+    if (blockIdx.x == 0 && tid == 0) a.starts[a.nq] = total;
+    __syncthreads();
+    if (u >= all) return;
+  }
+  const int64_t all = total * a.groups, run = (all + a.n_cta - 1) / a.n_cta;
+  const int64_t u_begin = (int64_t)blockIdx.x * run, u_end = min(u_begin + run, all);
+  const int Hq = a.Hkv * a.G;
+
+  int qi = item_s;
+  int64_t q_start = item_start_s * a.groups;       // first unit of the query, over its groups
+  for (int64_t u = u_begin; u < u_end;) {
+    const int32_t pos = __ldg(a.query_pos + qi);
+    const UnitRange ur = unit_range(pos, a.window, a.n_sink);
+    if (u >= q_start + (int64_t)ur.count * a.groups) {     // on to the next query (or past empty ones)
+      q_start += (int64_t)ur.count * a.groups;
+      ++qi;
+      continue;
+    }
+    const int grp = (int)((u - q_start) / ur.count);
+    const int64_t i_start = q_start + (int64_t)grp * ur.count, i_end = i_start + ur.count;
+    const int32_t c0 = (int32_t)(u - i_start), c1 = (int32_t)(min(u_end, i_end) - i_start);
+    const int32_t seq = a.seq_of_query ? __ldg(a.seq_of_query + qi) : qi;
+
+    // ---- this warp's head and tiles
+    const int vh0 = grp * a.per_cta, n_vh = min(a.per_cta, a.vh - vh0);
+    const int share = kGqaWarps / n_vh;            // warps per virtual head
+    const int vh = vh0 + warp / share, sub = warp % share;
+    const bool busy = warp < n_vh * share;
+    const int head = vh / a.subs, r0 = (vh % a.subs) * 8 * NT;
+    const int heads = min(8 * NT, a.G - r0);
+    GqaState<D, NT> st;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      st.mo[n][0] = st.mo[n][1] = -INFINITY;
+      st.l[n][0] = st.l[n][1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) st.o[n][j][0] = st.o[n][j][1] = st.o[n][j][2] = st.o[n][j][3] = 0.f;
+    }
+    if (busy) {
+      uint32_t qf[NT][D / 16][2];
+      float qs[NT][2];
+      load_query<D, NT>(a, a.q + ((int64_t)qi * Hq + head * a.G + r0) * D, heads, g, t, qf, qs);
+      constexpr int TPU = kUnit / 16;
+      const int32_t t1 = c1 * TPU;
+      auto row_of = [&](int32_t x) { return ur.row(x / TPU) + (x % TPU) * 16; };
+      auto next = [&](int32_t x) {                 // the next tile of this warp with a row to see
+        while (x < t1 && !sees_any(row_of(x), 16, pos, a.window, a.n_sink)) x += share;
+        return x;
+      };
+      auto fetch = [&](int32_t x, GqaTile<D>& kv) {
+        int64_t r[4];
+        const int32_t p0 = row_of(x);
+        if (tile_rows(a, seq, p0, pos, r)) {
+          load_tile<D>(a, kv, r, p0, pos, head, g, t);
+          return true;
+        }
+        record_error(a.status, CSA2_ERR_INDEX_RANGE);
+        return false;
+      };
+      int32_t x = next(c0 * TPU + sub);
+      GqaTile<D> kv[2];
+      bool have = x < t1 && fetch(x, kv[0]);
+      while (x < t1) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          if (x < t1) {
+            const int32_t y = next(x + share);
+            const bool have_y = y < t1 && fetch(y, kv[b ^ 1]);
+            if (have) tile_step<D, NT>(a, st, kv[b], qf, qs, row_of(x), pos, g);
+            x = y;
+            have = have_y;
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) st.l[n][e] += __shfl_xor_sync(0xffffffffu, st.l[n][e], o);
+    }
+    // ---- warps of the same head join
+    if (share > 1) {
+      constexpr int W = D + 2;                     // O, maximum, sum
+      if (busy && sub > 0) {
+        float* m = merge_s + (size_t)warp * 8 * NT * W;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float* hm = m + (n * 8 + 2 * t + e) * W;
+            if (g == 0) hm[D] = st.mo[n][e], hm[D + 1] = st.l[n][e];
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              hm[g * (D / 8) + 2 * j] = st.o[n][j][e];
+              hm[g * (D / 8) + 2 * j + 1] = st.o[n][j][2 + e];
+            }
+          }
+      }
+      __syncthreads();
+      if (busy && sub == 0) {
+        for (int w = 1; w < share; ++w) {
+          const float* m = merge_s + (size_t)(warp + w) * 8 * NT * W;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float* hm = m + (n * 8 + 2 * t + e) * W;
+              const float mo = fmaxf(st.mo[n][e], hm[D]);
+              const float f0 = st.mo[n][e] == -INFINITY ? (st.l[n][e] != st.l[n][e] ? st.l[n][e] : 0.f) : ex2(st.mo[n][e] - mo);
+              const float f1 = hm[D] == -INFINITY ? (hm[D + 1] != hm[D + 1] ? hm[D + 1] : 0.f) : ex2(hm[D] - mo);
+              st.mo[n][e] = mo;
+              st.l[n][e] = st.l[n][e] * f0 + hm[D + 1] * f1;
+#pragma unroll
+              for (int j = 0; j < D / 16; ++j) {
+                st.o[n][j][e] = st.o[n][j][e] * f0 + hm[g * (D / 8) + 2 * j] * f1;
+                st.o[n][j][2 + e] = st.o[n][j][2 + e] * f0 + hm[g * (D / 8) + 2 * j + 1] * f1;
+              }
+            }
+        }
+      }
+      __syncthreads();
+    }
+    // ---- the whole item: its output; else this CTA's part of it
+    if (busy && sub == 0) {
+      const bool before = i_start < u_begin, after = i_end > u_end;
+      const int rows = a.per_cta * 8 * NT;
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (before ? 0 : 1);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = n * 8 + 2 * t + e;
+          if (r >= heads) continue;
+          float v[D / 8];
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) v[2 * j] = st.o[n][j][e], v[2 * j + 1] = st.o[n][j][2 + e];
+          if (!before && !after) {
+            const int64_t at = (int64_t)qi * Hq + head * a.G + r0 + r;
+            store_bf16<D>(a.out + at * D + g * (D / 8), v, st.l[n][e] == 0.f ? 0.f : 1.f / st.l[n][e]);
+            if (a.lse && g == 0)
+              a.lse[at] = st.l[n][e] == 0.f ? -INFINITY : (st.mo[n][e] + log2f(st.l[n][e])) * 0.69314718055994531f;
+          } else {
+            const int64_t at = slot * rows + (vh - vh0) * 8 * NT + r;
+#pragma unroll
+            for (int j = 0; j < D / 32; ++j)
+              reinterpret_cast<float4*>(a.part_o + at * D + g * (D / 8))[j] =
+                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            if (g == 0) a.part_ml[at] = make_float2(st.mo[n][e], st.l[n][e]);
+          }
+        }
+    }
+    u = i_start + c1;
+  }
+}
+
+// Joins the parts of every item that several CTAs share, and writes the
+// outputs of queries that see no row.  One block per (query, virtual head).
+constexpr int kCombThreads = 128;
+constexpr int kCombWarps = kCombThreads / 32;
+template <int D>
+__global__ void __launch_bounds__(kCombThreads) gqa_combine_kernel(const __grid_constant__ GqaArgs a, int32_t run_heads) {
+  __shared__ float acc_s[kCombWarps][D];
+  __shared__ float m_s[kCombWarps], l_s[kCombWarps];
+  const int r = blockIdx.x, qi = blockIdx.y;           // query head, query
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t pos = __ldg(a.query_pos + qi);
+  const int32_t count = unit_range(pos, a.window, a.n_sink).count;
+  const int64_t at = (int64_t)qi * (a.Hkv * a.G) + r;
+  pdl_wait();
+  if (count == 0) {
+    for (int i = threadIdx.x; i < D / 2; i += kCombThreads) reinterpret_cast<uint32_t*>(a.out + at * D)[i] = 0u;
+    if (threadIdx.x == 0 && a.lse) a.lse[at] = -INFINITY;
+    return;
+  }
+  const int vh = (r / a.G) * a.subs + (r % a.G) / run_heads, grp = vh / a.per_cta;
+  const int64_t all = __ldcg(a.starts + a.nq) * a.groups, run = (all + a.n_cta - 1) / a.n_cta;
+  const int64_t i0 = __ldcg(a.starts + qi) * a.groups + (int64_t)grp * count, i1 = i0 + count;
+  const int64_t first = i0 / run, last = (i1 - 1) / run;
+  if (first == last) return;                           // one CTA had the whole item
+  const int rows = a.per_cta * run_heads, row = (vh - grp * a.per_cta) * run_heads + (r % a.G) % run_heads;
+  auto part = [&](int64_t c) { return (2 * c + (c == first ? 1 : 0)) * rows + row; };
+  float M = -INFINITY;
+  for (int64_t c = first + threadIdx.x; c <= last; c += kCombThreads) M = fmaxf(M, __ldcg(&a.part_ml[part(c)]).x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  if (lane == 0) m_s[warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kCombWarps; ++w) M = fmaxf(M, m_s[w]);
+  constexpr int V = D / 32;                            // values per lane
+  float acc[V], l = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll 4
+  for (int64_t c = first + warp; c <= last; c += kCombWarps) {
+    const int64_t p = part(c);
+    const float2 ml = __ldcg(&a.part_ml[p]);
+    const float f = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - M);
+    const float* o = a.part_o + p * D + lane * V;
+    l += f * ml.y;
+    if constexpr (V == 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(o));
+      acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(o));
+      acc[0] += f * v.x, acc[1] += f * v.y;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc_s[warp][lane * V + i] = acc[i];
+  if (lane == 0) l_s[warp] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < kCombWarps; ++w) l += l_s[w];
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  for (int i = threadIdx.x; i < D; i += kCombThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kCombWarps; ++w) v += acc_s[w][i];
+    reinterpret_cast<__nv_bfloat16*>(a.out)[at * D + i] = __float2bfloat16_rn(v * inv);
+  }
+  if (threadIdx.x == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
+}
+
+constexpr int kMaxCtas = 2 * 160;      // main-kernel CTAs at most: the workspace is sized without a device
+
+template <int D, int NT>
+cudaError_t launch_gqa_t(GqaArgs& a, cudaStream_t st) {
+  static SetupMask done{0};
+  // several warps of a head leave their states in shared memory
+  const int share = kGqaWarps / (a.vh < a.per_cta ? a.vh : a.per_cta);
+  const size_t smem = share > 1 || a.vh % a.per_cta ? (size_t)kGqaWarps * 8 * NT * (D + 2) * 4 : 0;
+  cudaError_t e = ensure_smem(gqa_split_kernel<D, NT>, kGqaWarps * 8 * NT * (D + 2) * 4, done);
+  if (e != cudaSuccess) return e;
+  a.n_cta = sm_count() * (NT == 1 ? 2 : 1);
+  if (a.n_cta > kMaxCtas) a.n_cta = kMaxCtas;
+  gqa_split_kernel<D, NT><<<a.n_cta, kGqaThreads, smem, st>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_k(gqa_combine_kernel<D>, dim3(a.Hkv * a.G, a.nq), dim3(kCombThreads), 0, st, false, true, a,
+                  (int32_t)(8 * NT));
+}
+
+// How query heads map to warps: runs of 8 NT heads of a KV head, up to 8 runs per CTA.
+void gqa_heads(GqaArgs& a, int32_t Hkv, int32_t G, int* nt) {
+  *nt = G <= 8 ? 1 : 2;
+  a.Hkv = Hkv;
+  a.G = G;
+  a.subs = (G + 8 * *nt - 1) / (8 * *nt);
+  a.vh = Hkv * a.subs;
+  a.groups = (a.vh + kGqaWarps - 1) / kGqaWarps;
+  a.per_cta = (a.vh + a.groups - 1) / a.groups;
+}
+
+void carve_gqa(GqaArgs& a, Carver& c, int32_t nq, int32_t D, int nt) {
+  const size_t parts = 2 * (size_t)kMaxCtas * a.per_cta * 8 * nt;
+  a.starts = c.take<int64_t>((size_t)nq + 1);
+  a.part_o = c.take<float>(parts * D);
+  a.part_ml = c.take<float2>(parts);
+}
+
+}  // namespace
+
+size_t gqa_scratch_bytes(int32_t nq, int32_t Hq, int32_t Hkv, int32_t D) {
+  GqaArgs a{};
+  int nt;
+  gqa_heads(a, Hkv, Hq / Hkv, &nt);
+  Carver c(nullptr);
+  carve_gqa(a, c, nq, D, nt);
+  return c.used + 256;
+}
+
+cudaError_t launch_gqa_attn(const uint16_t* q, const csa2_kv_cache& kv, const int32_t* seq_of_query,
+                            const int32_t* query_pos, int32_t nq, int32_t Hq, int32_t window, int32_t n_sink,
+                            float scale, bool group_queries, uint16_t* out, float* lse, void* ws, int32_t* status,
+                            cudaStream_t st) {
+  (void)group_queries;
+  GqaArgs a{};
+  int nt;
+  gqa_heads(a, kv.Hkv, Hq / kv.Hkv, &nt);
+  Carver c(ws);
+  carve_gqa(a, c, nq, kv.D, nt);
+  a.q = q, a.out = out, a.lse = lse;
+  const csa2_rows* views[4] = {&kv.k_codes, &kv.k_scales, &kv.v_codes, &kv.v_scales};
+  a.one_map = 1;
+  for (int i = 0; i < 4; ++i) {
+    a.base[i] = static_cast<const uint8_t*>(views[i]->base);
+    a.rb[i] = views[i]->row_bytes;
+    a.map[i] = to_rowmap(*views[i]);
+    if (!same_rows(*views[0], *views[i])) a.one_map = 0;
+  }
+  a.seq_of_query = seq_of_query;
+  a.query_pos = query_pos;
+  a.nq = nq;
+  a.window = window;
+  a.n_sink = window > 0 ? n_sink : 0;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.status = status;
+  if (kv.D == 128) return nt == 1 ? launch_gqa_t<128, 1>(a, st) : launch_gqa_t<128, 2>(a, st);
+  return nt == 1 ? launch_gqa_t<64, 1>(a, st) : launch_gqa_t<64, 2>(a, st);
+}
+
+}  // namespace csa2

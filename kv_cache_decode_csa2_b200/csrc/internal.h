@@ -246,6 +246,23 @@ cudaError_t launch_fp4_quantize(const void* x, bool bf16, int64_t n_rows, int32_
                                 uint8_t* scales, int64_t ld_scales, int64_t n_dst_rows,
                                 int32_t* status, cudaStream_t st);
 
+// Append of keys and values to the grouped-query FP4 cache with rotation
+// (kv_append.cu).  f32: the inputs are fp32, else bf16.
+cudaError_t launch_kv_append(const void* q, const void* k, const void* v, bool f32, int32_t n, int32_t Hq,
+                             int64_t ld_q, int64_t ld_k, int64_t ld_v, const int32_t* seq_of_row,
+                             const int32_t* row_pos, const float* cos_sin, int64_t n_pos, int32_t rot,
+                             bool interleaved, const csa2_kv_cache& cache, uint16_t* q_out, uint16_t* k_out,
+                             uint16_t* v_out, int32_t* status, cudaStream_t st);
+
+// Grouped-query attention over the FP4 cache (gqa_attn.cu).
+size_t gqa_scratch_bytes(int32_t nq, int32_t Hq, int32_t Hkv, int32_t D);
+cudaError_t launch_gqa_attn(const uint16_t* q, const csa2_kv_cache& cache, const int32_t* seq_of_query,
+                            const int32_t* query_pos, int32_t nq, int32_t Hq, int32_t window, int32_t n_sink,
+                            float scale, bool group_queries, uint16_t* out, float* lse, void* ws, int32_t* status,
+                            cudaStream_t st);
+// Whether two views place the rows of every (sequence, position) alike.
+bool same_rows(const csa2_rows& x, const csa2_rows& y);
+
 int sm_count();
 
 // Self-test of the bounded waits (selftest.cu).

@@ -33,6 +33,7 @@
 #include <cuda_fp16.h>
 
 #include "csa2_device.cuh"
+#include "fp4_device.cuh"
 #include "internal.h"
 #include "select_common.cuh"
 
@@ -82,37 +83,6 @@ struct AttnArgs {
   AttnLocal local[kMaxJobs];
 };
 static_assert(sizeof(AttnArgs) <= 4096, "kernel parameters");
-
-// Two E2M1 codes (low nibble = first element) -> f16x2, exactly (every E2M1
-// value is an f16 value).
-__device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t byte) {
-  uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.u8.u32 t, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}" : "=r"(r) : "r"(byte));
-  return r;
-}
-// One E4M3 byte -> the f16x2 pair (s, s), exactly (E4M3 spans 2^-9..448).
-__device__ __forceinline__ uint32_t e4m3_to_f16x2_pair(uint32_t byte) {
-  uint32_t r;
-  const uint16_t two = (uint16_t)(byte | (byte << 8));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
-  return r;
-}
-// Four packed codes (8 elements) times their block scale -> 4 bf16x2 words.
-// The f16 product is exact (at most 6 significant bits, between 2^-10 and
-// 2688), and so is its bf16 copy.
-__device__ __forceinline__ void dequant8(uint32_t codes, uint32_t scale_byte, uint32_t (&out)[4]) {
-  const __half2 s2 = __halves2half2(__ushort_as_half((uint16_t)(e4m3_to_f16x2_pair(scale_byte) & 0xFFFFu)),
-                                    __ushort_as_half((uint16_t)(e4m3_to_f16x2_pair(scale_byte) & 0xFFFFu)));
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const uint32_t h = e2m1x2_to_f16x2((codes >> (8 * e)) & 0xFFu);
-    __half2 v = *reinterpret_cast<const __half2*>(&h);
-    v = __hmul2(v, s2);
-    const float2 f = __half22float2(v);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-    out[e] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-}
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"

@@ -54,6 +54,10 @@ see tests/test_oracle_pins.py):
                       attends to are READINGS 3 and 4 (parity unpinned by the
                       pages).
   prefill_query       pinned: equals decode at the same position (property).
+  rotate_heads        pinned: multiplication of complex numbers.
+  visible_rows        pinned: the definition position by position.
+  gqa_attention       pinned: torch scaled_dot_product_attention (fp64), and
+                      sparse_attention when one head is its own value.
   attention_combine   pinned: equals sparse_attention over the union on random
                       partitions (one set empty), and the single-set identity.
   kv_rows_local_window  pinned: closed forms (one window row, uniform
@@ -435,3 +439,59 @@ def prefill_query(q, w, keys, q_attn, codes, scales, pos: int, topk: int, window
     kv = fp4_dequant(codes[S], scales[S], np.asarray(q_attn).shape[1])
     o, lse = sparse_attention(q_attn, kv, softmax_scale)
     return sel, S, o, lse
+
+
+# =============================================================== grouped-query layers
+def rotate_heads(x: np.ndarray, cos: np.ndarray, sin: np.ndarray, interleaved: bool) -> np.ndarray:
+    """Turns the first 2m values of every head by its token's m angles.
+
+    x [n][H][D], cos and sin [n][m].  Pair i is (2i, 2i + 1) if interleaved,
+    else (i, i + m), and (a, b) becomes (a cos - b sin, b cos + a sin).  The
+    arithmetic is that of x's type (float32 here means one rounding per
+    product and per sum).
+    """
+    m = cos.shape[1]
+    y = np.array(x, copy=True)
+    ia, ib = (np.arange(0, 2 * m, 2), np.arange(1, 2 * m, 2)) if interleaved else (np.arange(m), np.arange(m, 2 * m))
+    a, b = x[:, :, ia], x[:, :, ib]
+    c, s = cos[:, None, :].astype(x.dtype), sin[:, None, :].astype(x.dtype)
+    y[:, :, ia] = a * c - b * s
+    y[:, :, ib] = b * c + a * s
+    return y
+
+
+def visible_rows(pos: int, window: int = 0, n_sink: int = 0) -> np.ndarray:
+    """Ascending positions a query at `pos` sees: all up to pos, or with a
+    window the last `window` of them and the first n_sink."""
+    p = np.arange(pos + 1, dtype=np.int64)
+    return p[(p > pos - window) | (p < n_sink)] if window > 0 else p
+
+
+def gqa_attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, softmax_scale: float | None = None):
+    """Softmax attention of one query over m rows, query head h on KV head
+    h // (Hq / Hkv).  q [Hq][D], k and v [m][Hkv][D], in float64.
+
+    Returns (o [Hq][D], lse [Hq], spread [Hq][D], reach [Hq], total [Hq][D]):
+    besides the result, sum_j p_j |v_j|, scale max_j sum_d |q_d k_jd| and
+    sum_j |v_j|, to which relative errors of the weights, errors of the logits
+    and absolute errors of the weights are proportional.  With no row, o is 0
+    and the lse -inf.
+    """
+    q, k, v = (np.asarray(t, dtype=np.float64) for t in (q, k, v))
+    Hq, D = q.shape
+    if k.shape[0] == 0:
+        return np.zeros((Hq, D)), np.full(Hq, -np.inf), np.zeros((Hq, D)), np.zeros(Hq), np.zeros((Hq, D))
+    if softmax_scale is None or softmax_scale <= 0:
+        softmax_scale = 1.0 / math.sqrt(D)
+    G = Hq // k.shape[1]
+    o, lse, spread, reach = np.empty((Hq, D)), np.empty(Hq), np.empty((Hq, D)), np.empty(Hq)
+    total = np.repeat(np.abs(v).sum(0), G, axis=0)
+    for h in range(Hq):
+        kh, vh = k[:, h // G], v[:, h // G]
+        s = softmax_scale * (kh @ q[h])
+        e = np.exp(s - s.max())
+        p = e / e.sum()
+        o[h], spread[h] = p @ vh, p @ np.abs(vh)
+        lse[h] = s.max() + math.log(e.sum())
+        reach[h] = softmax_scale * (np.abs(kh) @ np.abs(q[h])).max()
+    return o, lse, spread, reach, total
