@@ -64,70 +64,130 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// One 16-row tile of a KV head as a lane holds it: codes of rows g and g + 8
-// of K, of rows 2t, 2t + 1, 2t + 8, 2t + 9 of V, and their scales.
+// A warp's ring of tiles in shared memory.  A tile is 16 rows of one KV head:
+// K codes as they are (a lane reads its quarter row), V codes with rows 0, 2, 4,
+// 6 next to one another, then 1, 3, 5, 7 and so on (the rows a quad reads at
+// once fill the banks; at D = 128 every other pair of rows has its halves
+// swapped for the same end), and four bytes of scales per row.
+constexpr int kStages = 4;
 template <int D>
-struct GqaTile {
-  uint32_t k[2][D / 32];
-  uint32_t v[4][D / 64];
-  uint32_t ks, vs;            // scale bytes: of K in bytes 0 and 1, of V in bytes 0 to 3
+struct GqaRing {
+  static constexpr int kRow = D / 2;
+  static constexpr int k = 0, v = 16 * kRow, sc = 32 * kRow;
+  static constexpr int stage = 32 * kRow + 128;
+  static constexpr int warp = kStages * stage;
+};
+template <int D>
+__device__ __forceinline__ int v_at(int row, int byte) {       // of a byte of V row `row` in its tile
+  const int slot = ((row >> 1) & 3) + 4 * ((row & 1) + 2 * (row >> 3));
+  return slot * (D / 2) + (D == 128 ? byte ^ (((slot >> 1) & 1) << 5) : byte);
+}
+
+// Copies 16 bytes to shared memory, or zeroes them.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// The page of unit u in a plane (0 where it is contiguous, -1 past the table).
+__device__ __forceinline__ int32_t unit_page(const RowMap& m, int32_t seq, int32_t u) {
+  if (!m.page_table) return 0;
+  const int32_t pg = u / (m.page_rows / kUnit);
+  return seq < 0 || pg >= m.max_pages ? -1 : __ldg(m.page_table + (int64_t)seq * m.max_pages + pg);
+}
+// First physical row of unit u, whose rows up to `last` (a position) are
+// wanted; -1 when they are not all in the plane.
+__device__ __forceinline__ int64_t unit_base(const RowMap& m, int32_t seq, int32_t u, int32_t page, int32_t last) {
+  const int32_t n = min(kUnit - 1, last - u * kUnit);
+  int64_t r;
+  if (m.page_table) {
+    const int32_t pu = m.page_rows / kUnit;
+    r = page < 0 ? -1 : (int64_t)page * m.page_rows + (u - u / pu * pu) * kUnit;
+  } else {
+    r = seq < 0 || (m.seq_rows > 0 && u * kUnit + n >= m.seq_rows) ? -1 : (int64_t)seq * m.seq_rows + (int64_t)u * kUnit;
+  }
+  return r >= 0 && r + n < m.n_rows ? r : -1;
+}
+
+// Where a lane's parts of the tiles come from: it copies 16 bytes of one or
+// two rows of K and of V, and loads one row's scales (K in lanes 0 to 15, V
+// above).  Pages are looked up a unit ahead.
+template <int D>
+struct GqaSource {
+  static constexpr int kPer = D / 32;             // lanes per row
+  const GqaArgs& a;
+  int32_t seq, pos, head, lane;
+  int32_t unit = -1, ahead = -1;                  // whose rows k, v, s are; whose pages are loaded
+  int32_t page[3];
+  const uint8_t *k, *v, *s;                       // this lane's parts of row 0 of the unit
+  bool ok = false;
+  __device__ __forceinline__ GqaSource(const GqaArgs& args, int32_t sq, int32_t p, int32_t h, int l)
+      : a(args), seq(sq), pos(p), head(h), lane(l) {}
+  __device__ __forceinline__ int s_plane() const { return lane < 16 ? 1 : 3; }
+  __device__ __forceinline__ void look_up(int32_t u) {
+    ahead = u;
+    page[0] = unit_page(a.map[0], seq, u);
+    if (!a.one_map) {
+      page[1] = unit_page(a.map[2], seq, u);
+      page[2] = unit_page(a.map[s_plane()], seq, u);
+    }
+  }
+  // Moves to unit u; `then` (or -1) is the one after it.
+  __device__ __forceinline__ void go(int32_t u, int32_t then) {
+    if (ahead != u) look_up(u);
+    unit = u;
+    const int64_t rk = unit_base(a.map[0], seq, u, page[0], pos);
+    const int64_t rv = a.one_map ? rk : unit_base(a.map[2], seq, u, page[1], pos);
+    const int64_t rs = a.one_map ? rk : unit_base(a.map[s_plane()], seq, u, page[2], pos);
+    ok = !__any_sync(0xffffffffu, rk < 0 || rv < 0 || rs < 0);
+    if (!ok && lane == 0) record_error(a.status, CSA2_ERR_INDEX_RANGE);
+    const int row = lane / kPer, byte = (lane % kPer) * 16;
+    k = a.base[0] + (rk + row) * a.rb[0] + head * (D / 2) + byte;
+    v = a.base[2] + (rv + row) * a.rb[2] + head * (D / 2) + byte;
+    const int sp = s_plane();
+    s = a.base[sp] + (rs + (lane & 15)) * a.rb[sp] + head * (D / 32);
+    if (then >= 0) look_up(then);
+  }
+  // Starts the copies of tile i of the unit into `stage`; returns its scales.
+  __device__ __forceinline__ uint32_t copy(int i, uint32_t stage) const {
+    const int p0 = unit * kUnit + 16 * i, row = lane / kPer, byte = (lane % kPer) * 16;
+    const bool full = sees_all(p0);
+#pragma unroll
+    for (int x = 0; x < 16; x += 32 / kPer) {
+      const bool take = full || sees(p0 + row + x, pos, a.window, a.n_sink);
+      const int64_t at = 16 * i + x;
+      copy16(stage + GqaRing<D>::k + (row + x) * (D / 2) + byte, take ? k + at * a.rb[0] : a.base[0], take);
+      copy16(stage + GqaRing<D>::v + v_at<D>(row + x, byte), take ? v + at * a.rb[2] : a.base[2], take);
+    }
+    if (!full && !sees(p0 + (lane & 15), pos, a.window, a.n_sink)) return 0;
+    const uint8_t* p = s + (int64_t)(16 * i) * a.rb[s_plane()];
+    return D == 128 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p));
+  }
+  __device__ __forceinline__ bool sees_all(int32_t p0) const {
+    return p0 + 15 <= pos && (a.window <= 0 || p0 > pos - a.window || p0 + 15 < a.n_sink);
+  }
 };
 
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t r;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(at));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t at) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(at));
+  return r;
+}
 template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
-  if constexpr (N == 4) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-  } else if constexpr (N == 2) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-    w[0] = u.x, w[1] = u.y;
-  } else {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-  }
-}
-
-// First physical row of the tile at position p0 in each plane; false (and the
-// error recorded) when the rows up to `last` are not all in the plane.
-__device__ __forceinline__ bool tile_rows(const GqaArgs& a, int32_t seq, int32_t p0, int32_t last, int64_t (&r)[4]) {
-  const int32_t n = min(15, last - p0);
-  bool ok = true;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i > 0 && a.one_map) {
-      r[i] = r[0];
-      continue;
-    }
-    const RowMap& m = a.map[i];
-    r[i] = seq < 0 || (!m.page_table && m.seq_rows > 0 && p0 + n >= m.seq_rows) ? -1 : map_row(m, seq, p0);
-    ok = ok && r[i] >= 0 && r[i] + n < m.n_rows;
-  }
-  return ok;
-}
-
-template <int D>
-__device__ __forceinline__ void load_tile(const GqaArgs& a, GqaTile<D>& x, const int64_t (&r)[4], int32_t p0,
-                                          int32_t pos, int head, int g, int t) {
-  x.ks = x.vs = 0;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int m = g + 8 * i;
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) x.k[i][w] = 0;
-    if (sees(p0 + m, pos, a.window, a.n_sink)) {
-      load_words(a.base[0] + (r[0] + m) * a.rb[0] + head * (D / 2) + t * (D / 8), x.k[i]);
-      x.ks |= (uint32_t)__ldg(a.base[1] + (r[1] + m) * a.rb[1] + head * (D / 32) + t * (D / 4) / 32) << (8 * i);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m = 2 * t + (i & 1) + 8 * (i >> 1);
-#pragma unroll
-    for (int w = 0; w < D / 64; ++w) x.v[i][w] = 0;
-    if (sees(p0 + m, pos, a.window, a.n_sink)) {
-      load_words(a.base[2] + (r[2] + m) * a.rb[2] + head * (D / 2) + g * (D / 16), x.v[i]);
-      x.vs |= (uint32_t)__ldg(a.base[3] + (r[3] + m) * a.rb[3] + head * (D / 32) + g * (D / 8) / 32) << (8 * i);
-    }
-  }
+__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
+  if constexpr (N == 4)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
+  else if constexpr (N == 2)
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+  else
+    w[0] = lds32(at);
 }
 
 // Running state of a warp: NT runs of 8 heads.  A lane holds heads 2t and
@@ -139,33 +199,48 @@ struct GqaState {
   float l[NT][2];             // this lane's part of the sum of weights
 };
 
+// One tile: S^T = K Q^T, the weights, O^T += V^T P^T.  `full`: every row is seen.
 template <int D, int NT>
-__device__ __forceinline__ void tile_step(const GqaArgs& a, GqaState<D, NT>& st, const GqaTile<D>& x,
-                                          const uint32_t (&qf)[NT][D / 16][2], const float (&qs)[NT][2], int32_t p0,
-                                          int32_t pos, int g) {
+__device__ __forceinline__ void tile_step(const GqaArgs& a, GqaState<D, NT>& st, uint32_t stage,
+                                          const uint32_t (&qf)[NT][D / 16][2], const float (&qs)[NT][2], bool full,
+                                          int32_t p0, int32_t pos, int g, int t) {
+  using R = GqaRing<D>;
   float s[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-  const uint32_t sk0 = e4m3x2_to_f16x2(__byte_perm(x.ks, 0, 0x0000)), sk1 = e4m3x2_to_f16x2(__byte_perm(x.ks, 0, 0x1111));
+  {
+    uint32_t k0[D / 32], k1[D / 32];
+    lds_words(stage + R::k + g * R::kRow + t * (D / 8), k0);
+    lds_words(stage + R::k + (g + 8) * R::kRow + t * (D / 8), k1);
+    const uint32_t sk0 = e4m3x2_to_f16x2(lds8(stage + R::sc + g * 4 + t * (D / 4) / 32) * 0x101u);
+    const uint32_t sk1 = e4m3x2_to_f16x2(lds8(stage + R::sc + (g + 8) * 4 + t * (D / 4) / 32) * 0x101u);
 #pragma unroll
-  for (int k = 0; k < D / 16; ++k) {
-    const uint32_t w0 = x.k[0][k / 2] >> (16 * (k & 1)), w1 = x.k[1][k / 2] >> (16 * (k & 1));
-    const uint32_t af[4] = {mul_f16x2(e2m1x2_to_f16x2(w0 & 0xFFu), sk0), mul_f16x2(e2m1x2_to_f16x2(w1 & 0xFFu), sk1),
-                            mul_f16x2(e2m1x2_to_f16x2((w0 >> 8) & 0xFFu), sk0),
-                            mul_f16x2(e2m1x2_to_f16x2((w1 >> 8) & 0xFFu), sk1)};
+    for (int k = 0; k < D / 16; ++k) {
+      const uint32_t w0 = k0[k / 2] >> (16 * (k & 1)), w1 = k1[k / 2] >> (16 * (k & 1));
+      const uint32_t af[4] = {mul_f16x2(e2m1x2_to_f16x2(w0 & 0xFFu), sk0), mul_f16x2(e2m1x2_to_f16x2(w1 & 0xFFu), sk1),
+                              mul_f16x2(e2m1x2_to_f16x2((w0 >> 8) & 0xFFu), sk0),
+                              mul_f16x2(e2m1x2_to_f16x2((w1 >> 8) & 0xFFu), sk1)};
 #pragma unroll
-    for (int n = 0; n < NT; ++n) mma_f16(s[n], af, qf[n][k][0], qf[n][k][1]);
+      for (int n = 0; n < NT; ++n) mma_f16(s[n], af, qf[n][k][0], qf[n][k][1]);
+    }
   }
-  const bool see0 = sees(p0 + g, pos, a.window, a.n_sink), see1 = sees(p0 + g + 8, pos, a.window, a.n_sink);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[n][i] *= qs[n][i & 1];
+  if (!full) {
+    const bool see0 = sees(p0 + g, pos, a.window, a.n_sink), see1 = sees(p0 + g + 8, pos, a.window, a.n_sink);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!(i < 2 ? see0 : see1)) s[n][i] = -INFINITY;
+  }
   bool more = false;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      s[n][e] = see0 ? s[n][e] * qs[n][e] : -INFINITY;
-      s[n][2 + e] = see1 ? s[n][2 + e] * qs[n][e] : -INFINITY;
-      more |= fmaxf(s[n][e], s[n][2 + e]) > st.mo[n][e] + (kOffset + kLazy);
-    }
+    for (int e = 0; e < 2; ++e) more |= fmaxf(s[n][e], s[n][2 + e]) > st.mo[n][e] + (kOffset + kLazy);
   if (__any_sync(0xffffffffu, more)) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -200,14 +275,19 @@ __device__ __forceinline__ void tile_step(const GqaArgs& a, GqaState<D, NT>& st,
       pf[n][i] = transpose8x8(*reinterpret_cast<const uint32_t*>(&h));
     }
   }
-  const uint32_t sv0 = e4m3x2_to_f16x2(x.vs), sv1 = e4m3x2_to_f16x2(x.vs >> 16);
+  uint32_t v[4][D / 64], sv[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = 2 * t + (i & 1) + 8 * (i >> 1);
+    lds_words(stage + R::v + v_at<D>(row, g * (D / 16)), v[i]);
+    sv[i] = lds8(stage + R::sc + 64 + row * 4 + g * (D / 8) / 32);
+  }
+  const uint32_t sv0 = e4m3x2_to_f16x2(sv[0] | sv[1] << 8), sv1 = e4m3x2_to_f16x2(sv[2] | sv[3] << 8);
 #pragma unroll
   for (int w = 0; w < D / 64; ++w) {
     constexpr uint32_t kLow = 0x0F0F0F0Fu;
-    const uint32_t lo01 = (x.v[0][w] & kLow) | ((x.v[1][w] & kLow) << 4);
-    const uint32_t hi01 = ((x.v[0][w] >> 4) & kLow) | (x.v[1][w] & ~kLow);
-    const uint32_t lo23 = (x.v[2][w] & kLow) | ((x.v[3][w] & kLow) << 4);
-    const uint32_t hi23 = ((x.v[2][w] >> 4) & kLow) | (x.v[3][w] & ~kLow);
+    const uint32_t lo01 = (v[0][w] & kLow) | ((v[1][w] << 4) & ~kLow), hi01 = ((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow);
+    const uint32_t lo23 = (v[2][w] & kLow) | ((v[3][w] << 4) & ~kLow), hi23 = ((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
       const uint32_t af[4] = {mul_f16x2(e2m1x2_to_f16x2((lo01 >> (8 * b)) & 0xFFu), sv0),
@@ -292,7 +372,7 @@ __device__ __forceinline__ void store_bf16(uint16_t* dst, const float* v, float 
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel(const __grid_constant__ GqaArgs a) {
-  extern __shared__ __align__(16) float merge_s[];     // [warps][8 NT][D + 2] when several warps share a head
+  extern __shared__ __align__(128) uint8_t gqa_s[];    // the warps' rings; then [warps][8 NT][D + 2] floats to join
   __shared__ int64_t scan_s[kGqaWarps];
   __shared__ int32_t item_s;
   __shared__ int64_t item_start_s;
@@ -362,38 +442,54 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
       uint32_t qf[NT][D / 16][2];
       float qs[NT][2];
       load_query<D, NT>(a, a.q + ((int64_t)qi * Hq + head * a.G + r0) * D, heads, g, t, qf, qs);
+      // tiles c0 * 4 + sub, + share, ... that hold a row to see: kStages - 1 of
+      // them in flight while one is worked on
       constexpr int TPU = kUnit / 16;
       const int32_t t1 = c1 * TPU;
-      auto row_of = [&](int32_t x) { return ur.row(x / TPU) + (x % TPU) * 16; };
-      auto next = [&](int32_t x) {                 // the next tile of this warp with a row to see
-        while (x < t1 && !sees_any(row_of(x), 16, pos, a.window, a.n_sink)) x += share;
+      const uint32_t ring = smem_u32(gqa_s) + warp * GqaRing<D>::warp;
+      auto unit_of = [&](int32_t x) { return ur.row(x / TPU) / kUnit; };
+      auto next = [&](int32_t x) {
+        while (x < t1 && !sees_any(ur.row(x / TPU) + (x % TPU) * 16, 16, pos, a.window, a.n_sink)) x += share;
         return x;
       };
-      auto fetch = [&](int32_t x, GqaTile<D>& kv) {
-        int64_t r[4];
-        const int32_t p0 = row_of(x);
-        if (tile_rows(a, seq, p0, pos, r)) {
-          load_tile<D>(a, kv, r, p0, pos, head, g, t);
-          return true;
-        }
-        record_error(a.status, CSA2_ERR_INDEX_RANGE);
-        return false;
-      };
-      int32_t x = next(c0 * TPU + sub);
-      GqaTile<D> kv[2];
-      bool have = x < t1 && fetch(x, kv[0]);
-      while (x < t1) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          if (x < t1) {
-            const int32_t y = next(x + share);
-            const bool have_y = y < t1 && fetch(y, kv[b ^ 1]);
-            if (have) tile_step<D, NT>(a, st, kv[b], qf, qs, row_of(x), pos, g);
-            x = y;
-            have = have_y;
+      GqaSource<D> src(a, seq, pos, head, lane);
+      int32_t load = next(c0 * TPU + sub), work = load;
+      uint32_t sc = 0, bad = 0;                    // scales on their way; stages whose rows are not there
+      int ls = 0, ws = 0;
+      auto start = [&]() {                         // starts the next tile's copies; its stage's scales come back
+        if (load < t1) {
+          const int32_t u = unit_of(load);
+          if (u != src.unit) {
+            const int32_t then = (load / TPU + 1) * TPU;
+            src.go(u, then < t1 ? unit_of(then) : -1);
           }
+          bad = src.ok ? bad & ~(1u << ls) : bad | (1u << ls);
+          sc = src.ok ? src.copy(load % TPU, ring + ls * GqaRing<D>::stage) : 0;
+          load = next(load + share);
         }
+        copies_commit();
+      };
+      auto put_scales = [&]() {
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(ring + ls * GqaRing<D>::stage + GqaRing<D>::sc + lane * 4), "r"(sc)
+                     : "memory");
+        ls = ls + 1 == kStages ? 0 : ls + 1;
+      };
+#pragma unroll
+      for (int i = 0; i < kStages - 2; ++i) start(), put_scales();
+      start();
+      while (work < t1) {
+        copies_wait<kStages - 2>();
+        __syncwarp();                              // the tile is there, and its predecessor's stage is free
+        put_scales();
+        start();
+        const int32_t p0 = ur.row(work / TPU) + (work % TPU) * 16;
+        if (!((bad >> ws) & 1u))
+          tile_step<D, NT>(a, st, ring + ws * GqaRing<D>::stage, qf, qs, src.sees_all(p0), p0, pos, g, t);
+        ws = ws + 1 == kStages ? 0 : ws + 1;
+        work = next(work + share);
       }
+      copies_wait<0>();
+      __syncwarp();
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -404,6 +500,8 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
     // ---- warps of the same head join
     if (share > 1) {
       constexpr int W = D + 2;                     // O, maximum, sum
+      float* merge_s = reinterpret_cast<float*>(gqa_s);
+      __syncthreads();                             // the rings are done with
       if (busy && sub > 0) {
         float* m = merge_s + (size_t)warp * 8 * NT * W;
 #pragma unroll
@@ -551,10 +649,9 @@ constexpr int kMaxCtas = 2 * 160;      // main-kernel CTAs at most: the workspac
 template <int D, int NT>
 cudaError_t launch_gqa_t(GqaArgs& a, cudaStream_t st) {
   static SetupMask done{0};
-  // several warps of a head leave their states in shared memory
-  const int share = kGqaWarps / (a.vh < a.per_cta ? a.vh : a.per_cta);
-  const size_t smem = share > 1 || a.vh % a.per_cta ? (size_t)kGqaWarps * 8 * NT * (D + 2) * 4 : 0;
-  cudaError_t e = ensure_smem(gqa_split_kernel<D, NT>, kGqaWarps * 8 * NT * (D + 2) * 4, done);
+  constexpr size_t rings = (size_t)kGqaWarps * GqaRing<D>::warp, join = (size_t)kGqaWarps * 8 * NT * (D + 2) * 4;
+  constexpr size_t smem = rings > join ? rings : join;
+  cudaError_t e = ensure_smem(gqa_split_kernel<D, NT>, (int)smem, done);
   if (e != cudaSuccess) return e;
   a.n_cta = sm_count() * (NT == 1 ? 2 : 1);
   if (a.n_cta > kMaxCtas) a.n_cta = kMaxCtas;
