@@ -365,7 +365,7 @@ int32_t csa2_fp4_quantize_bf16(const uint16_t* x, int64_t n_rows, int32_t D, int
  * The cache: Hkv key heads and Hkv value heads of D values per position, in
  * four planes.  A code row holds the heads one after another, D/2 bytes each
  * (row_bytes >= Hkv D/2, a multiple of 16); a scale row D/32 bytes each
- * (row_bytes >= Hkv D/32, a multiple of D/32).  Paged or contiguous as every
+ * (row_bytes >= Hkv D/32, a multiple of D/32); row_bytes <= 2^24.  Paged or contiguous as every
  * csa2_rows; a position at or past seq_rows of a contiguous plane whose
  * seq_rows is not 0 is out of range (CSA2_ERR_INDEX_RANGE).  The planes may be
  * the same memory (keys that are their own values).

@@ -304,6 +304,8 @@ static bool kv_shape_ok(int32_t Hq, int32_t Hkv, int32_t D) {
   return (D == 64 || D == 128) && Hkv >= 1 && Hkv <= 256 && Hq >= 0 && Hq <= 1024;
 }
 static bool kv_cache_ok(const csa2_kv_cache* c) {
+  for (const csa2_rows* v : {&c->k_codes, &c->k_scales, &c->v_codes, &c->v_scales})
+    if (v->row_bytes > 1 << 24) return false;
   return rows_ok(&c->k_codes, (int64_t)c->Hkv * c->D / 2, 16) && rows_ok(&c->v_codes, (int64_t)c->Hkv * c->D / 2, 16) &&
          rows_ok(&c->k_scales, (int64_t)c->Hkv * c->D / 32, c->D / 32) &&
          rows_ok(&c->v_scales, (int64_t)c->Hkv * c->D / 32, c->D / 32);

@@ -53,6 +53,19 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+// Eight codes to four f16 pairs, in order.  The bytes are taken apart by name
+// (mov.b32), which the conversion reads in place: 81 values per clock and SM
+// with the multiply by the scale, against 43 with shifts and masks.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
+}
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
@@ -92,19 +105,22 @@ template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // The page of unit u in a plane (0 where it is contiguous, -1 past the table).
-__device__ __forceinline__ int32_t unit_page(const RowMap& m, int32_t seq, int32_t u) {
+__device__ __forceinline__ int32_t page_of(const RowMap& m, int32_t shift, int32_t u) {
+  return shift >= 0 ? u >> shift : u / (m.page_rows / kUnit);
+}
+__device__ __forceinline__ int32_t unit_page(const RowMap& m, int32_t shift, int32_t seq, int32_t u) {
   if (!m.page_table) return 0;
-  const int32_t pg = u / (m.page_rows / kUnit);
+  const int32_t pg = page_of(m, shift, u);
   return seq < 0 || pg >= m.max_pages ? -1 : __ldg(m.page_table + (int64_t)seq * m.max_pages + pg);
 }
 // First physical row of unit u, whose rows up to `last` (a position) are
 // wanted; -1 when they are not all in the plane.
-__device__ __forceinline__ int64_t unit_base(const RowMap& m, int32_t seq, int32_t u, int32_t page, int32_t last) {
+__device__ __forceinline__ int64_t unit_base(const RowMap& m, int32_t shift, int32_t seq, int32_t u, int32_t page,
+                                             int32_t last) {
   const int32_t n = min(kUnit - 1, last - u * kUnit);
   int64_t r;
   if (m.page_table) {
-    const int32_t pu = m.page_rows / kUnit;
-    r = page < 0 ? -1 : (int64_t)page * m.page_rows + (u - u / pu * pu) * kUnit;
+    r = page < 0 ? -1 : (int64_t)page * m.page_rows + (u * kUnit - page_of(m, shift, u) * m.page_rows);
   } else {
     r = seq < 0 || (m.seq_rows > 0 && u * kUnit + n >= m.seq_rows) ? -1 : (int64_t)seq * m.seq_rows + (int64_t)u * kUnit;
   }
@@ -122,25 +138,26 @@ struct GqaSource {
   int32_t unit = -1, ahead = -1;                  // whose rows k, v, s are; whose pages are loaded
   int32_t page[3];
   const uint8_t *k, *v, *s;                       // this lane's parts of row 0 of the unit
+  uint32_t srb;                                   // row stride of its scale plane
   bool ok = false;
   __device__ __forceinline__ GqaSource(const GqaArgs& args, int32_t sq, int32_t p, int32_t h, int l)
-      : a(args), seq(sq), pos(p), head(h), lane(l) {}
+      : a(args), seq(sq), pos(p), head(h), lane(l), srb((uint32_t)args.rb[s_plane()]) {}
   __device__ __forceinline__ int s_plane() const { return lane < 16 ? 1 : 3; }
   __device__ __forceinline__ void look_up(int32_t u) {
     ahead = u;
-    page[0] = unit_page(a.map[0], seq, u);
+    page[0] = unit_page(a.map[0], a.page_shift[0], seq, u);
     if (!a.one_map) {
-      page[1] = unit_page(a.map[2], seq, u);
-      page[2] = unit_page(a.map[s_plane()], seq, u);
+      page[1] = unit_page(a.map[2], a.page_shift[2], seq, u);
+      page[2] = unit_page(a.map[s_plane()], a.page_shift[s_plane()], seq, u);
     }
   }
   // Moves to unit u; `then` (or -1) is the one after it.
   __device__ __forceinline__ void go(int32_t u, int32_t then) {
     if (ahead != u) look_up(u);
     unit = u;
-    const int64_t rk = unit_base(a.map[0], seq, u, page[0], pos);
-    const int64_t rv = a.one_map ? rk : unit_base(a.map[2], seq, u, page[1], pos);
-    const int64_t rs = a.one_map ? rk : unit_base(a.map[s_plane()], seq, u, page[2], pos);
+    const int64_t rk = unit_base(a.map[0], a.page_shift[0], seq, u, page[0], pos);
+    const int64_t rv = a.one_map ? rk : unit_base(a.map[2], a.page_shift[2], seq, u, page[1], pos);
+    const int64_t rs = a.one_map ? rk : unit_base(a.map[s_plane()], a.page_shift[s_plane()], seq, u, page[2], pos);
     ok = !__any_sync(0xffffffffu, rk < 0 || rv < 0 || rs < 0);
     if (!ok && lane == 0) record_error(a.status, CSA2_ERR_INDEX_RANGE);
     const int row = lane / kPer, byte = (lane % kPer) * 16;
@@ -157,12 +174,12 @@ struct GqaSource {
 #pragma unroll
     for (int x = 0; x < 16; x += 32 / kPer) {
       const bool take = full || sees(p0 + row + x, pos, a.window, a.n_sink);
-      const int64_t at = 16 * i + x;
-      copy16(stage + GqaRing<D>::k + (row + x) * (D / 2) + byte, take ? k + at * a.rb[0] : a.base[0], take);
-      copy16(stage + GqaRing<D>::v + v_at<D>(row + x, byte), take ? v + at * a.rb[2] : a.base[2], take);
+      const uint32_t at = 16 * i + x;
+      copy16(stage + GqaRing<D>::k + (row + x) * (D / 2) + byte, k + (uint64_t)at * (uint32_t)a.rb[0], take);
+      copy16(stage + GqaRing<D>::v + v_at<D>(row + x, byte), v + (uint64_t)at * (uint32_t)a.rb[2], take);
     }
     if (!full && !sees(p0 + (lane & 15), pos, a.window, a.n_sink)) return 0;
-    const uint8_t* p = s + (int64_t)(16 * i) * a.rb[s_plane()];
+    const uint8_t* p = s + (uint64_t)(uint32_t)(16 * i) * srb;
     return D == 128 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p));
   }
   __device__ __forceinline__ bool sees_all(int32_t p0) const {
@@ -215,45 +232,46 @@ __device__ __forceinline__ void tile_step(const GqaArgs& a, GqaState<D, NT>& st,
     const uint32_t sk0 = e4m3x2_to_f16x2(lds8(stage + R::sc + g * 4 + t * (D / 4) / 32) * 0x101u);
     const uint32_t sk1 = e4m3x2_to_f16x2(lds8(stage + R::sc + (g + 8) * 4 + t * (D / 4) / 32) * 0x101u);
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t w0 = k0[k / 2] >> (16 * (k & 1)), w1 = k1[k / 2] >> (16 * (k & 1));
-      const uint32_t af[4] = {mul_f16x2(e2m1x2_to_f16x2(w0 & 0xFFu), sk0), mul_f16x2(e2m1x2_to_f16x2(w1 & 0xFFu), sk1),
-                              mul_f16x2(e2m1x2_to_f16x2((w0 >> 8) & 0xFFu), sk0),
-                              mul_f16x2(e2m1x2_to_f16x2((w1 >> 8) & 0xFFu), sk1)};
+    for (int w = 0; w < D / 32; ++w) {
+      uint32_t x0[4], x1[4];
+      e2m1x8_to_f16(k0[w], x0);
+      e2m1x8_to_f16(k1[w], x1);
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma_f16(s[n], af, qf[n][k][0], qf[n][k][1]);
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t af[4] = {mul_f16x2(x0[2 * h], sk0), mul_f16x2(x1[2 * h], sk1), mul_f16x2(x0[2 * h + 1], sk0),
+                                mul_f16x2(x1[2 * h + 1], sk1)};
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mma_f16(s[n], af, qf[n][2 * w + h][0], qf[n][2 * w + h][1]);
+      }
     }
   }
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[n][i] *= qs[n][i & 1];
-  if (!full) {
-    const bool see0 = sees(p0 + g, pos, a.window, a.n_sink), see1 = sees(p0 + g + 8, pos, a.window, a.n_sink);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (!(i < 2 ? see0 : see1)) s[n][i] = -INFINITY;
-  }
+  // x = the logit above the maximum in use, plus kOffset
+  const bool see0 = full || sees(p0 + g, pos, a.window, a.n_sink);
+  const bool see1 = full || sees(p0 + g + 8, pos, a.window, a.n_sink);
+  float x[NT][4];
   bool more = false;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) more |= fmaxf(s[n][e], s[n][2 + e]) > st.mo[n][e] + (kOffset + kLazy);
+    for (int i = 0; i < 4; ++i) {
+      x[n][i] = (i < 2 ? see0 : see1) ? fmaf(s[n][i], qs[n][i & 1], -st.mo[n][i & 1]) : -INFINITY;
+      more |= x[n][i] > kOffset + kLazy;
+    }
   if (__any_sync(0xffffffffu, more)) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float f[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float m = fmaxf(s[n][e], s[n][2 + e]);
+        float m = fmaxf(see0 ? s[n][e] * qs[n][e] : -INFINITY, see1 ? s[n][2 + e] * qs[n][e] : -INFINITY);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float mo = fmaxf(st.mo[n][e], m - kOffset);
         f[e] = st.mo[n][e] == -INFINITY ? 0.f : ex2(st.mo[n][e] - mo);
         st.mo[n][e] = mo;
         st.l[n][e] *= f[e];
+        x[n][e] = see0 ? fmaf(s[n][e], qs[n][e], -mo) : -INFINITY;
+        x[n][2 + e] = see1 ? fmaf(s[n][2 + e], qs[n][e], -mo) : -INFINITY;
       }
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
@@ -266,7 +284,7 @@ __device__ __forceinline__ void tile_step(const GqaArgs& a, GqaState<D, NT>& st,
   for (int n = 0; n < NT; ++n) {
     float p[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = ex2(s[n][i] - st.mo[n][i & 1]);
+    for (int i = 0; i < 4; ++i) p[i] = ex2(x[n][i]);
     st.l[n][0] += p[0] + p[2];
     st.l[n][1] += p[1] + p[3];
 #pragma unroll
@@ -288,12 +306,14 @@ __device__ __forceinline__ void tile_step(const GqaArgs& a, GqaState<D, NT>& st,
     constexpr uint32_t kLow = 0x0F0F0F0Fu;
     const uint32_t lo01 = (v[0][w] & kLow) | ((v[1][w] << 4) & ~kLow), hi01 = ((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow);
     const uint32_t lo23 = (v[2][w] & kLow) | ((v[3][w] << 4) & ~kLow), hi23 = ((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow);
+    uint32_t x0[4], x1[4], x2[4], x3[4];
+    e2m1x8_to_f16(lo01, x0);
+    e2m1x8_to_f16(hi01, x1);
+    e2m1x8_to_f16(lo23, x2);
+    e2m1x8_to_f16(hi23, x3);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-      const uint32_t af[4] = {mul_f16x2(e2m1x2_to_f16x2((lo01 >> (8 * b)) & 0xFFu), sv0),
-                              mul_f16x2(e2m1x2_to_f16x2((hi01 >> (8 * b)) & 0xFFu), sv0),
-                              mul_f16x2(e2m1x2_to_f16x2((lo23 >> (8 * b)) & 0xFFu), sv1),
-                              mul_f16x2(e2m1x2_to_f16x2((hi23 >> (8 * b)) & 0xFFu), sv1)};
+      const uint32_t af[4] = {mul_f16x2(x0[b], sv0), mul_f16x2(x1[b], sv0), mul_f16x2(x2[b], sv1), mul_f16x2(x3[b], sv1)};
 #pragma unroll
       for (int n = 0; n < NT; ++n) mma_f16(st.o[n][4 * w + b], af, pf[n][0], pf[n][1]);
     }
@@ -445,11 +465,11 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
       // tiles c0 * 4 + sub, + share, ... that hold a row to see: kStages - 1 of
       // them in flight while one is worked on
       constexpr int TPU = kUnit / 16;
-      const int32_t t1 = c1 * TPU;
+      const int32_t t1 = c1 == ur.count ? (c1 - 1) * TPU + pos % kUnit / 16 + 1 : c1 * TPU;   // none past pos
       const uint32_t ring = smem_u32(gqa_s) + warp * GqaRing<D>::warp;
       auto unit_of = [&](int32_t x) { return ur.row(x / TPU) / kUnit; };
       auto next = [&](int32_t x) {
-        while (x < t1 && !sees_any(ur.row(x / TPU) + (x % TPU) * 16, 16, pos, a.window, a.n_sink)) x += share;
+        if (a.window > 0) while (x < t1 && !sees_any(ur.row(x / TPU) + (x % TPU) * 16, 16, pos, a.window, a.n_sink)) x += share;
         return x;
       };
       GqaSource<D> src(a, seq, pos, head, lane);
@@ -709,6 +729,10 @@ cudaError_t launch_gqa_attn(const uint16_t* q, const csa2_kv_cache& kv, const in
     a.rb[i] = views[i]->row_bytes;
     a.map[i] = to_rowmap(*views[i]);
     if (!same_rows(*views[0], *views[i])) a.one_map = 0;
+    const int32_t units = views[i]->page_table ? views[i]->page_rows / kUnit : 1;
+    a.page_shift[i] = -1;
+    for (int b = 0; b < 31; ++b)
+      if (units == 1 << b) a.page_shift[i] = b;
   }
   a.seq_of_query = seq_of_query;
   a.query_pos = query_pos;

@@ -26,6 +26,7 @@ struct GqaArgs {
   const uint8_t* base[4];          // K codes, K scales, V codes, V scales
   int64_t rb[4];
   RowMap map[4];
+  int32_t page_shift[4];           // log2 of the units per page (-1: not a power of two)
   int32_t one_map;                 // all four planes place rows alike
   const int32_t* seq_of_query;
   const int32_t* query_pos;
