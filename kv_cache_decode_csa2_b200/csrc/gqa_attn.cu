@@ -38,7 +38,7 @@ constexpr float kLazy = 5.f;          // how far a logit may exceed the maximum 
 constexpr float kOffset = 10.f;       // weights are 2^(s - m + kOffset)
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -46,7 +46,7 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
 // Transposes an 8 x 8 matrix of 16-bit values held as two per lane.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
@@ -77,17 +77,18 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// A warp's ring of tiles in shared memory.  A tile is 16 rows of one KV head:
-// K codes as they are (a lane reads its quarter row), V codes with rows 0, 2, 4,
-// 6 next to one another, then 1, 3, 5, 7 and so on (the rows a quad reads at
-// once fill the banks; at D = 128 every other pair of rows has its halves
-// swapped for the same end), and four bytes of scales per row.
-constexpr int kStages = 4;
+// A warp's ring of tiles in shared memory.  A tile is kRows rows of one KV
+// head: K codes as they are (a lane reads its quarter row), V codes of every 16
+// rows with rows 0, 2, 4, 6 next to one another, then 1, 3, 5, 7 and so on (the
+// rows a quad reads at once fill the banks; at D = 128 every other pair of rows
+// has its halves swapped for the same end), and four bytes of scales per row.
+constexpr int kRows = 32;
+constexpr int kStages = 3;
 template <int D>
 struct GqaRing {
   static constexpr int kRow = D / 2;
-  static constexpr int k = 0, v = 16 * kRow, sc = 32 * kRow;
-  static constexpr int stage = 32 * kRow + 128;
+  static constexpr int k = 0, v = kRows * kRow, ks = 2 * kRows * kRow, vs = ks + 4 * kRows;
+  static constexpr int stage = vs + 4 * kRows;
   static constexpr int warp = kStages * stage;
 };
 template <int D>
@@ -104,107 +105,99 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-// The page of unit u in a plane (0 where it is contiguous, -1 past the table).
-__device__ __forceinline__ int32_t page_of(const RowMap& m, int32_t shift, int32_t u) {
-  return shift >= 0 ? u >> shift : u / (m.page_rows / kUnit);
+// The page of row p in a plane (0 where it is contiguous, -1 past the table).
+__device__ __forceinline__ int32_t page_of(const RowMap& m, int32_t shift, int32_t p) {
+  return shift >= 0 ? p >> shift : p / m.page_rows;
 }
-__device__ __forceinline__ int32_t unit_page(const RowMap& m, int32_t shift, int32_t seq, int32_t u) {
+__device__ __forceinline__ int32_t load_page(const RowMap& m, int32_t shift, int32_t seq, int32_t p) {
   if (!m.page_table) return 0;
-  const int32_t pg = page_of(m, shift, u);
+  const int32_t pg = page_of(m, shift, p);
   return seq < 0 || pg >= m.max_pages ? -1 : __ldg(m.page_table + (int64_t)seq * m.max_pages + pg);
 }
-// First physical row of unit u, whose rows up to `last` (a position) are
-// wanted; -1 when they are not all in the plane.
-__device__ __forceinline__ int64_t unit_base(const RowMap& m, int32_t shift, int32_t seq, int32_t u, int32_t page,
+// Physical row of position p (a multiple of kPageStep), of whose step the
+// rows up to position `last` are wanted; -1 when they are not all in the plane.
+__device__ __forceinline__ int64_t step_base(const RowMap& m, int32_t shift, int32_t seq, int32_t p, int32_t page,
                                              int32_t last) {
-  const int32_t n = min(kUnit - 1, last - u * kUnit);
+  const int32_t n = min(kPageStep - 1, last - p);
   int64_t r;
-  if (m.page_table) {
-    r = page < 0 ? -1 : (int64_t)page * m.page_rows + (u * kUnit - page_of(m, shift, u) * m.page_rows);
-  } else {
-    r = seq < 0 || (m.seq_rows > 0 && u * kUnit + n >= m.seq_rows) ? -1 : (int64_t)seq * m.seq_rows + (int64_t)u * kUnit;
-  }
+  if (m.page_table)
+    r = page < 0 ? -1 : (int64_t)page * m.page_rows + (p - page_of(m, shift, p) * m.page_rows);
+  else
+    r = seq < 0 || (m.seq_rows > 0 && p + n >= m.seq_rows) ? -1 : (int64_t)seq * m.seq_rows + p;
   return r >= 0 && r + n < m.n_rows ? r : -1;
 }
 
-// Where a lane's parts of the tiles come from: it copies 16 bytes of one or
-// two rows of K and of V, and loads one row's scales (K in lanes 0 to 15, V
-// above).  Pages are looked up a unit ahead.
+// Where a lane's parts of the tiles come from: it copies 16 bytes of every
+// 32 / kPer-th row of K and of V, and loads the scales of row `lane` of both.
+// Pages are looked up a step ahead.
 template <int D>
 struct GqaSource {
   static constexpr int kPer = D / 32;             // lanes per row
   const GqaArgs& a;
-  int32_t seq, pos, head, lane;
-  int32_t unit = -1, ahead = -1;                  // whose rows k, v, s are; whose pages are loaded
-  int32_t page[3];
-  const uint8_t *k, *v, *s;                       // this lane's parts of row 0 of the unit
-  uint32_t srb;                                   // row stride of its scale plane
+  int32_t seq, last, head, lane;
+  int32_t step = -1, ahead = -1;                  // first row of the step at hand; of the one looked up
+  int32_t page[4];
+  const uint8_t* at[4];                           // this lane's parts of row 0 of the step
   bool ok = false;
   __device__ __forceinline__ GqaSource(const GqaArgs& args, int32_t sq, int32_t p, int32_t h, int l)
-      : a(args), seq(sq), pos(p), head(h), lane(l), srb((uint32_t)args.rb[s_plane()]) {}
-  __device__ __forceinline__ int s_plane() const { return lane < 16 ? 1 : 3; }
-  __device__ __forceinline__ void look_up(int32_t u) {
-    ahead = u;
-    page[0] = unit_page(a.map[0], a.page_shift[0], seq, u);
-    if (!a.one_map) {
-      page[1] = unit_page(a.map[2], a.page_shift[2], seq, u);
-      page[2] = unit_page(a.map[s_plane()], a.page_shift[s_plane()], seq, u);
-    }
+      : a(args), seq(sq), last(p), head(h), lane(l) {}
+  __device__ __forceinline__ void look_up(int32_t p) {
+    ahead = p;
+    page[0] = load_page(a.map[0], a.page_shift[0], seq, p);
+    if (!a.one_map)
+#pragma unroll
+      for (int i = 1; i < 4; ++i) page[i] = load_page(a.map[i], a.page_shift[i], seq, p);
   }
-  // Moves to unit u; `then` (or -1) is the one after it.
-  __device__ __forceinline__ void go(int32_t u, int32_t then) {
-    if (ahead != u) look_up(u);
-    unit = u;
-    const int64_t rk = unit_base(a.map[0], a.page_shift[0], seq, u, page[0], pos);
-    const int64_t rv = a.one_map ? rk : unit_base(a.map[2], a.page_shift[2], seq, u, page[1], pos);
-    const int64_t rs = a.one_map ? rk : unit_base(a.map[s_plane()], a.page_shift[s_plane()], seq, u, page[2], pos);
-    ok = !__any_sync(0xffffffffu, rk < 0 || rv < 0 || rs < 0);
+  // Moves to the step at row p; `then` (or -1) is the one after it.
+  __device__ __forceinline__ void go(int32_t p, int32_t then) {
+    if (ahead != p) look_up(p);
+    step = p;
+    int64_t r = 0;
+    ok = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i == 0 || !a.one_map) r = step_base(a.map[i], a.page_shift[i], seq, p, page[i], last);
+      ok = ok && r >= 0;
+      at[i] = a.base[i] + (r + (i & 1 ? lane : lane / kPer)) * a.rb[i] +
+              (i & 1 ? head * (D / 32) : head * (D / 2) + (lane % kPer) * 16);
+    }
     if (!ok && lane == 0) record_error(a.status, CSA2_ERR_INDEX_RANGE);
-    const int row = lane / kPer, byte = (lane % kPer) * 16;
-    k = a.base[0] + (rk + row) * a.rb[0] + head * (D / 2) + byte;
-    v = a.base[2] + (rv + row) * a.rb[2] + head * (D / 2) + byte;
-    const int sp = s_plane();
-    s = a.base[sp] + (rs + (lane & 15)) * a.rb[sp] + head * (D / 32);
     if (then >= 0) look_up(then);
   }
-  // Starts the copies of tile i of the unit into `stage`; returns its scales.
-  __device__ __forceinline__ uint32_t copy(int i, uint32_t stage) const {
-    const int p0 = unit * kUnit + 16 * i, row = lane / kPer, byte = (lane % kPer) * 16;
-    const bool full = sees_all(p0);
-#pragma unroll
-    for (int x = 0; x < 16; x += 32 / kPer) {
-      const bool take = full || sees(p0 + row + x, pos, a.window, a.n_sink);
-      const uint32_t at = 16 * i + x;
-      copy16(stage + GqaRing<D>::k + (row + x) * (D / 2) + byte, k + (uint64_t)at * (uint32_t)a.rb[0], take);
-      copy16(stage + GqaRing<D>::v + v_at<D>(row + x, byte), v + (uint64_t)at * (uint32_t)a.rb[2], take);
-    }
-    if (!full && !sees(p0 + (lane & 15), pos, a.window, a.n_sink)) return 0;
-    const uint8_t* p = s + (uint64_t)(uint32_t)(16 * i) * srb;
+  __device__ __forceinline__ uint32_t scales(int i, uint32_t off) const {
+    const uint8_t* p = at[i] + (uint64_t)off * (uint32_t)a.rb[i];
     return D == 128 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p));
   }
-  __device__ __forceinline__ bool sees_all(int32_t p0) const {
-    return p0 + 15 <= pos && (a.window <= 0 || p0 > pos - a.window || p0 + 15 < a.n_sink);
+  // Starts the copies of the tile at row `off` of the step, whose rows w
+  // sees, into `stage`; ks and vs are the lane's scales.
+  __device__ __forceinline__ void copy(uint32_t off, uint32_t stage, const Seen& w, uint32_t& ks, uint32_t& vs) const {
+    const int row = lane / kPer, byte = (lane % kPer) * 16;
+    const bool full = w.all(kRows);
+#pragma unroll
+    for (int x = 0; x < kRows; x += 32 / kPer) {
+      const bool take = full || w.row(row + x);
+      copy16(stage + GqaRing<D>::k + (row + x) * (D / 2) + byte, at[0] + (uint64_t)(off + x) * (uint32_t)a.rb[0], take);
+      copy16(stage + GqaRing<D>::v + v_at<D>(row + x, byte), at[2] + (uint64_t)(off + x) * (uint32_t)a.rb[2], take);
+    }
+    ks = vs = 0;
+    if (full || w.row(lane)) {
+      ks = scales(1, off);
+      vs = scales(3, off);
+    }
   }
 };
 
-__device__ __forceinline__ uint32_t lds32(uint32_t at) {
-  uint32_t r;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(at));
-  return r;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t at) {
-  uint32_t r;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(at));
-  return r;
-}
 template <int N>
-__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
-  if constexpr (N == 4)
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at));
-  else if constexpr (N == 2)
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
-  else
-    w[0] = lds32(at);
+__device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+  } else if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x, w[1] = u.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
 }
 
 // Running state of a warp: NT runs of 8 heads.  A lane holds heads 2t and
@@ -216,62 +209,71 @@ struct GqaState {
   float l[NT][2];             // this lane's part of the sum of weights
 };
 
-// One tile: S^T = K Q^T, the weights, O^T += V^T P^T.  `full`: every row is seen.
+// One tile: S^T = K Q^T, the weights, O^T += V^T P^T; w: its rows that are seen.
 template <int D, int NT>
-__device__ __forceinline__ void tile_step(const GqaArgs& a, GqaState<D, NT>& st, uint32_t stage,
-                                          const uint32_t (&qf)[NT][D / 16][2], const float (&qs)[NT][2], bool full,
-                                          int32_t p0, int32_t pos, int g, int t) {
+__device__ __forceinline__ void tile_step(GqaState<D, NT>& st, const uint8_t* stage,
+                                          const uint32_t (&qf)[NT][D / 16][2], const float (&qs)[NT][2], const Seen& w,
+                                          int g, int t) {
   using R = GqaRing<D>;
-  float s[NT][4];
+  constexpr int H = kRows / 16;                    // MMA heights
+  float s[H][NT][4];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-  {
+  for (int h = 0; h < H; ++h) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n) s[h][n][0] = s[h][n][1] = s[h][n][2] = s[h][n][3] = 0.f;
+    const int r0 = 16 * h + g, r1 = r0 + 8;
     uint32_t k0[D / 32], k1[D / 32];
-    lds_words(stage + R::k + g * R::kRow + t * (D / 8), k0);
-    lds_words(stage + R::k + (g + 8) * R::kRow + t * (D / 8), k1);
-    const uint32_t sk0 = e4m3x2_to_f16x2(lds8(stage + R::sc + g * 4 + t * (D / 4) / 32) * 0x101u);
-    const uint32_t sk1 = e4m3x2_to_f16x2(lds8(stage + R::sc + (g + 8) * 4 + t * (D / 4) / 32) * 0x101u);
+    lds_words(stage + R::k + r0 * R::kRow + t * (D / 8), k0);
+    lds_words(stage + R::k + r1 * R::kRow + t * (D / 8), k1);
+    const uint32_t sk0 = e4m3x2_to_f16x2(stage[R::ks + r0 * 4 + t * (D / 4) / 32] * 0x101u);
+    const uint32_t sk1 = e4m3x2_to_f16x2(stage[R::ks + r1 * 4 + t * (D / 4) / 32] * 0x101u);
 #pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
+    for (int i = 0; i < D / 32; ++i) {
       uint32_t x0[4], x1[4];
-      e2m1x8_to_f16(k0[w], x0);
-      e2m1x8_to_f16(k1[w], x1);
+      e2m1x8_to_f16(k0[i], x0);
+      e2m1x8_to_f16(k1[i], x1);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t af[4] = {mul_f16x2(x0[2 * h], sk0), mul_f16x2(x1[2 * h], sk1), mul_f16x2(x0[2 * h + 1], sk0),
-                                mul_f16x2(x1[2 * h + 1], sk1)};
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t af[4] = {mul_f16x2(x0[2 * j], sk0), mul_f16x2(x1[2 * j], sk1), mul_f16x2(x0[2 * j + 1], sk0),
+                                mul_f16x2(x1[2 * j + 1], sk1)};
 #pragma unroll
-        for (int n = 0; n < NT; ++n) mma_f16(s[n], af, qf[n][2 * w + h][0], qf[n][2 * w + h][1]);
+        for (int n = 0; n < NT; ++n) mma_f16(s[h][n], af, qf[n][2 * i + j][0], qf[n][2 * i + j][1]);
       }
     }
   }
   // x = the logit above the maximum in use, plus kOffset
-  const bool see0 = full || sees(p0 + g, pos, a.window, a.n_sink);
-  const bool see1 = full || sees(p0 + g + 8, pos, a.window, a.n_sink);
-  float x[NT][4];
-  bool more = false;
+  bool see[2 * H];
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int i = 0; i < 2 * H; ++i) see[i] = w.row(g + 8 * i);
+  float x[H][NT][4];
+  float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[n][i] = (i < 2 ? see0 : see1) ? fmaf(s[n][i], qs[n][i & 1], -st.mo[n][i & 1]) : -INFINITY;
-      more |= x[n][i] > kOffset + kLazy;
-    }
-  if (__any_sync(0xffffffffu, more)) {
+  for (int h = 0; h < H; ++h)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[h][n][i] = see[2 * h + (i >> 1)] ? fmaf(s[h][n][i], qs[n][i & 1], -st.mo[n][i & 1]) : -INFINITY;
+        top = fmaxf(top, x[h][n][i]);
+      }
+  if (__any_sync(0xffffffffu, top > kOffset + kLazy)) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float f[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float m = fmaxf(see0 ? s[n][e] * qs[n][e] : -INFINITY, see1 ? s[n][2 + e] * qs[n][e] : -INFINITY);
+        float m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 2 * H; ++i) m = see[i] ? fmaxf(m, s[i >> 1][n][2 * (i & 1) + e] * qs[n][e]) : m;
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         const float mo = fmaxf(st.mo[n][e], m - kOffset);
         f[e] = st.mo[n][e] == -INFINITY ? 0.f : ex2(st.mo[n][e] - mo);
         st.mo[n][e] = mo;
         st.l[n][e] *= f[e];
-        x[n][e] = see0 ? fmaf(s[n][e], qs[n][e], -mo) : -INFINITY;
-        x[n][2 + e] = see1 ? fmaf(s[n][2 + e], qs[n][e], -mo) : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 2 * H; ++i)
+          x[i >> 1][n][2 * (i & 1) + e] = see[i] ? fmaf(s[i >> 1][n][2 * (i & 1) + e], qs[n][e], -mo) : -INFINITY;
       }
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
@@ -279,43 +281,45 @@ __device__ __forceinline__ void tile_step(const GqaArgs& a, GqaState<D, NT>& st,
         for (int i = 0; i < 4; ++i) st.o[n][j][i] *= f[i & 1];
     }
   }
-  uint32_t pf[NT][2];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    float p[4];
+  for (int h = 0; h < H; ++h) {
+    uint32_t pf[NT][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = ex2(x[n][i]);
-    st.l[n][0] += p[0] + p[2];
-    st.l[n][1] += p[1] + p[3];
+    for (int n = 0; n < NT; ++n) {
+      float p[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const __half2 h = __floats2half2_rn(p[2 * i], p[2 * i + 1]);
-      pf[n][i] = transpose8x8(*reinterpret_cast<const uint32_t*>(&h));
+      for (int i = 0; i < 4; ++i) p[i] = ex2(x[h][n][i]);
+      st.l[n][0] += p[0] + p[2];
+      st.l[n][1] += p[1] + p[3];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const __half2 hp = __floats2half2_rn(p[2 * i], p[2 * i + 1]);
+        pf[n][i] = transpose8x8(*reinterpret_cast<const uint32_t*>(&hp));
+      }
     }
-  }
-  uint32_t v[4][D / 64], sv[4];
+    uint32_t v[4][D / 64], sv[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = 2 * t + (i & 1) + 8 * (i >> 1);
-    lds_words(stage + R::v + v_at<D>(row, g * (D / 16)), v[i]);
-    sv[i] = lds8(stage + R::sc + 64 + row * 4 + g * (D / 8) / 32);
-  }
-  const uint32_t sv0 = e4m3x2_to_f16x2(sv[0] | sv[1] << 8), sv1 = e4m3x2_to_f16x2(sv[2] | sv[3] << 8);
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * h + 2 * t + (i & 1) + 8 * (i >> 1);
+      lds_words(stage + R::v + v_at<D>(row, g * (D / 16)), v[i]);
+      sv[i] = stage[R::vs + row * 4 + g * (D / 8) / 32];
+    }
+    const uint32_t sv0 = e4m3x2_to_f16x2(sv[0] | sv[1] << 8), sv1 = e4m3x2_to_f16x2(sv[2] | sv[3] << 8);
 #pragma unroll
-  for (int w = 0; w < D / 64; ++w) {
-    constexpr uint32_t kLow = 0x0F0F0F0Fu;
-    const uint32_t lo01 = (v[0][w] & kLow) | ((v[1][w] << 4) & ~kLow), hi01 = ((v[0][w] >> 4) & kLow) | (v[1][w] & ~kLow);
-    const uint32_t lo23 = (v[2][w] & kLow) | ((v[3][w] << 4) & ~kLow), hi23 = ((v[2][w] >> 4) & kLow) | (v[3][w] & ~kLow);
-    uint32_t x0[4], x1[4], x2[4], x3[4];
-    e2m1x8_to_f16(lo01, x0);
-    e2m1x8_to_f16(hi01, x1);
-    e2m1x8_to_f16(lo23, x2);
-    e2m1x8_to_f16(hi23, x3);
+    for (int c = 0; c < D / 64; ++c) {
+      constexpr uint32_t kLow = 0x0F0F0F0Fu;
+      uint32_t x0[4], x1[4], x2[4], x3[4];
+      e2m1x8_to_f16((v[0][c] & kLow) | ((v[1][c] << 4) & ~kLow), x0);
+      e2m1x8_to_f16(((v[0][c] >> 4) & kLow) | (v[1][c] & ~kLow), x1);
+      e2m1x8_to_f16((v[2][c] & kLow) | ((v[3][c] << 4) & ~kLow), x2);
+      e2m1x8_to_f16(((v[2][c] >> 4) & kLow) | (v[3][c] & ~kLow), x3);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const uint32_t af[4] = {mul_f16x2(x0[b], sv0), mul_f16x2(x1[b], sv0), mul_f16x2(x2[b], sv1), mul_f16x2(x3[b], sv1)};
+      for (int b = 0; b < 4; ++b) {
+        const uint32_t af[4] = {mul_f16x2(x0[b], sv0), mul_f16x2(x1[b], sv0), mul_f16x2(x2[b], sv1),
+                                mul_f16x2(x3[b], sv1)};
 #pragma unroll
-      for (int n = 0; n < NT; ++n) mma_f16(st.o[n][4 * w + b], af, pf[n][0], pf[n][1]);
+        for (int n = 0; n < NT; ++n) mma_f16(st.o[n][4 * c + b], af, pf[n][0], pf[n][1]);
+      }
     }
   }
 }
@@ -399,19 +403,19 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   pdl_trigger();
 
-  // ---- where this CTA's run of units starts
+  // ---- where this CTA's run of tiles starts
   int64_t total;
   {
     const int per = (a.nq + kGqaThreads - 1) / kGqaThreads;
     const int i0 = min(tid * per, a.nq), i1 = min(i0 + per, a.nq);
     int64_t n = 0;
-    for (int i = i0; i < i1; ++i) n += unit_range(__ldg(a.query_pos + i), a.window, a.n_sink).count;
+    for (int i = i0; i < i1; ++i) n += tile_range<kRows>(__ldg(a.query_pos + i), a.window, a.n_sink).count;
     int64_t start = block_scan(n, scan_s, &total);
     const int64_t all = total * a.groups, run = (all + a.n_cta - 1) / a.n_cta;
     const int64_t u = (int64_t)blockIdx.x * run;
     if (blockIdx.x == 0 || (start * a.groups <= u && u < (start + n) * a.groups)) {
       for (int i = i0; i < i1; ++i) {
-        const int64_t c = unit_range(__ldg(a.query_pos + i), a.window, a.n_sink).count;
+        const int64_t c = tile_range<kRows>(__ldg(a.query_pos + i), a.window, a.n_sink).count;
         if (blockIdx.x == 0) a.starts[i] = start;
         if (start * a.groups <= u && u < (start + c) * a.groups) {
           item_s = i;
@@ -429,10 +433,10 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
   const int Hq = a.Hkv * a.G;
 
   int qi = item_s;
-  int64_t q_start = item_start_s * a.groups;       // first unit of the query, over its groups
+  int64_t q_start = item_start_s * a.groups;       // first tile of the query, over its groups
   for (int64_t u = u_begin; u < u_end;) {
     const int32_t pos = __ldg(a.query_pos + qi);
-    const UnitRange ur = unit_range(pos, a.window, a.n_sink);
+    const TileRange ur = tile_range<kRows>(pos, a.window, a.n_sink);
     if (u >= q_start + (int64_t)ur.count * a.groups) {     // on to the next query (or past empty ones)
       q_start += (int64_t)ur.count * a.groups;
       ++qi;
@@ -462,51 +466,45 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
       uint32_t qf[NT][D / 16][2];
       float qs[NT][2];
       load_query<D, NT>(a, a.q + ((int64_t)qi * Hq + head * a.G + r0) * D, heads, g, t, qf, qs);
-      // tiles c0 * 4 + sub, + share, ... that hold a row to see: kStages - 1 of
-      // them in flight while one is worked on
-      constexpr int TPU = kUnit / 16;
-      const int32_t t1 = c1 == ur.count ? (c1 - 1) * TPU + pos % kUnit / 16 + 1 : c1 * TPU;   // none past pos
-      const uint32_t ring = smem_u32(gqa_s) + warp * GqaRing<D>::warp;
-      auto unit_of = [&](int32_t x) { return ur.row(x / TPU) / kUnit; };
-      auto next = [&](int32_t x) {
-        if (a.window > 0) while (x < t1 && !sees_any(ur.row(x / TPU) + (x % TPU) * 16, 16, pos, a.window, a.n_sink)) x += share;
-        return x;
-      };
+      // tiles c0 + sub, + share, ...: kStages - 1 of them in flight while one is worked on
+      uint8_t* ring_s = gqa_s + warp * GqaRing<D>::warp;
+      const uint32_t ring = smem_u32(ring_s);
+      const Seen seen = seen_rows(pos, a.window, a.n_sink);
       GqaSource<D> src(a, seq, pos, head, lane);
-      int32_t load = next(c0 * TPU + sub), work = load;
-      uint32_t sc = 0, bad = 0;                    // scales on their way; stages whose rows are not there
+      int32_t load = c0 + sub;
+      uint32_t ks = 0, vs = 0, bad = 0;            // scales on their way; stages whose rows are not there
       int ls = 0, ws = 0;
-      auto start = [&]() {                         // starts the next tile's copies; its stage's scales come back
-        if (load < t1) {
-          const int32_t u = unit_of(load);
-          if (u != src.unit) {
-            const int32_t then = (load / TPU + 1) * TPU;
-            src.go(u, then < t1 ? unit_of(then) : -1);
+      auto start = [&]() {                         // starts the next tile's copies; its scales come back
+        if (load < c1) {
+          const int32_t p0 = ur.row(load, kRows), step = p0 & ~(kPageStep - 1);
+          load += share;
+          if (step != src.step) {
+            // the step after it, by the last tile of this one's reach
+            const int32_t ahead = load + (kPageStep / kRows - 1) / share * share;
+            src.go(step, ahead < c1 ? ur.row(ahead, kRows) & ~(kPageStep - 1) : -1);
           }
           bad = src.ok ? bad & ~(1u << ls) : bad | (1u << ls);
-          sc = src.ok ? src.copy(load % TPU, ring + ls * GqaRing<D>::stage) : 0;
-          load = next(load + share);
+          if (src.ok) src.copy(p0 - step, ring + ls * GqaRing<D>::stage, seen.from(p0), ks, vs);
         }
         copies_commit();
       };
       auto put_scales = [&]() {
-        asm volatile("st.shared.b32 [%0], %1;" ::"r"(ring + ls * GqaRing<D>::stage + GqaRing<D>::sc + lane * 4), "r"(sc)
-                     : "memory");
+        uint32_t* to = reinterpret_cast<uint32_t*>(ring_s + ls * GqaRing<D>::stage + GqaRing<D>::ks) + lane;
+        to[0] = ks;
+        to[kRows] = vs;
         ls = ls + 1 == kStages ? 0 : ls + 1;
       };
 #pragma unroll
       for (int i = 0; i < kStages - 2; ++i) start(), put_scales();
       start();
-      while (work < t1) {
+      for (int32_t x = c0 + sub; x < c1; x += share) {
         copies_wait<kStages - 2>();
         __syncwarp();                              // the tile is there, and its predecessor's stage is free
         put_scales();
         start();
-        const int32_t p0 = ur.row(work / TPU) + (work % TPU) * 16;
         if (!((bad >> ws) & 1u))
-          tile_step<D, NT>(a, st, ring + ws * GqaRing<D>::stage, qf, qs, src.sees_all(p0), p0, pos, g, t);
+          tile_step<D, NT>(st, ring_s + ws * GqaRing<D>::stage, qf, qs, seen.from(ur.row(x, kRows)), g, t);
         ws = ws + 1 == kStages ? 0 : ws + 1;
-        work = next(work + share);
       }
       copies_wait<0>();
       __syncwarp();
@@ -605,7 +603,7 @@ __global__ void __launch_bounds__(kCombThreads) gqa_combine_kernel(const __grid_
   const int r = blockIdx.x, qi = blockIdx.y;           // query head, query
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t pos = __ldg(a.query_pos + qi);
-  const int32_t count = unit_range(pos, a.window, a.n_sink).count;
+  const int32_t count = tile_range<kRows>(pos, a.window, a.n_sink).count;
   const int64_t at = (int64_t)qi * (a.Hkv * a.G) + r;
   pdl_wait();
   if (count == 0) {
@@ -729,10 +727,9 @@ cudaError_t launch_gqa_attn(const uint16_t* q, const csa2_kv_cache& kv, const in
     a.rb[i] = views[i]->row_bytes;
     a.map[i] = to_rowmap(*views[i]);
     if (!same_rows(*views[0], *views[i])) a.one_map = 0;
-    const int32_t units = views[i]->page_table ? views[i]->page_rows / kUnit : 1;
     a.page_shift[i] = -1;
-    for (int b = 0; b < 31; ++b)
-      if (units == 1 << b) a.page_shift[i] = b;
+    for (int b = 6; b < 31; ++b)
+      if (views[i]->page_table && views[i]->page_rows == 1 << b) a.page_shift[i] = b;
   }
   a.seq_of_query = seq_of_query;
   a.query_pos = query_pos;
