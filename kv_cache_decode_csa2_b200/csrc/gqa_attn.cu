@@ -101,6 +101,9 @@ __device__ __forceinline__ int v_at(int row, int byte) {       // of a byte of V
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0) : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -172,15 +175,27 @@ struct GqaSource {
   // sees, into `stage`; ks and vs are the lane's scales.
   __device__ __forceinline__ void copy(uint32_t off, uint32_t stage, const Seen& w, uint32_t& ks, uint32_t& vs) const {
     const int row = lane / kPer, byte = (lane % kPer) * 16;
-    const bool full = w.all(kRows);
+    const uint8_t* k = at[0] + (uint64_t)off * (uint32_t)a.rb[0];
+    const uint8_t* v = at[2] + (uint64_t)off * (uint32_t)a.rb[2];
+    const uint32_t kd = stage + GqaRing<D>::k + row * (D / 2) + byte, vd = stage + GqaRing<D>::v + v_at<D>(row, byte);
+    constexpr int X = 32 / kPer;                  // 8 or 16 rows on, a tile's image moves by as many rows
+    if (w.all(kRows)) {
 #pragma unroll
-    for (int x = 0; x < kRows; x += 32 / kPer) {
-      const bool take = full || w.row(row + x);
-      copy16(stage + GqaRing<D>::k + (row + x) * (D / 2) + byte, at[0] + (uint64_t)(off + x) * (uint32_t)a.rb[0], take);
-      copy16(stage + GqaRing<D>::v + v_at<D>(row + x, byte), at[2] + (uint64_t)(off + x) * (uint32_t)a.rb[2], take);
+      for (int x = 0; x < kRows; x += X) {
+        copy16(kd + x * (D / 2), k + (uint64_t)x * (uint32_t)a.rb[0]);
+        copy16(vd + x * (D / 2), v + (uint64_t)x * (uint32_t)a.rb[2]);
+      }
+      ks = scales(1, off);
+      vs = scales(3, off);
+      return;
+    }
+    for (int x = 0; x < kRows; x += X) {
+      const bool take = w.row(row + x);
+      copy16(kd + x * (D / 2), k + (uint64_t)x * (uint32_t)a.rb[0], take);
+      copy16(vd + x * (D / 2), v + (uint64_t)x * (uint32_t)a.rb[2], take);
     }
     ks = vs = 0;
-    if (full || w.row(lane)) {
+    if (w.row(lane)) {
       ks = scales(1, off);
       vs = scales(3, off);
     }
@@ -244,7 +259,11 @@ __device__ __forceinline__ void tile_step(GqaState<D, NT>& st, const uint8_t* st
   // x = the logit above the maximum in use, plus kOffset
   bool see[2 * H];
 #pragma unroll
-  for (int i = 0; i < 2 * H; ++i) see[i] = w.row(g + 8 * i);
+  for (int i = 0; i < 2 * H; ++i) see[i] = true;
+  if (!w.all(kRows)) {
+#pragma unroll
+    for (int i = 0; i < 2 * H; ++i) see[i] = w.row(g + 8 * i);
+  }
   float x[H][NT][4];
   float top = -INFINITY;
 #pragma unroll
@@ -494,17 +513,20 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
         to[kRows] = vs;
         ls = ls + 1 == kStages ? 0 : ls + 1;
       };
-#pragma unroll
-      for (int i = 0; i < kStages - 2; ++i) start(), put_scales();
-      start();
-      for (int32_t x = c0 + sub; x < c1; x += share) {
-        copies_wait<kStages - 2>();
-        __syncwarp();                              // the tile is there, and its predecessor's stage is free
-        put_scales();
+      // kStages - 1 rounds that only start tiles, then one per tile
+      for (int32_t x = c0 + sub - (kStages - 1) * share; x < c1; x += share) {
+        const bool first = x < c0 + sub - (kStages - 2) * share;
+        if (x >= c0) {
+          copies_wait<kStages - 2>();
+          __syncwarp();                            // the tile is there, and its predecessor's stage is free
+        }
+        if (!first) put_scales();
         start();
-        if (!((bad >> ws) & 1u))
-          tile_step<D, NT>(st, ring_s + ws * GqaRing<D>::stage, qf, qs, seen.from(ur.row(x, kRows)), g, t);
-        ws = ws + 1 == kStages ? 0 : ws + 1;
+        if (x >= c0) {
+          if (!((bad >> ws) & 1u))
+            tile_step<D, NT>(st, ring_s + ws * GqaRing<D>::stage, qf, qs, seen.from(ur.row(x, kRows)), g, t);
+          ws = ws + 1 == kStages ? 0 : ws + 1;
+        }
       }
       copies_wait<0>();
       __syncwarp();
