@@ -377,6 +377,11 @@ __device__ __forceinline__ void load_query(const GqaArgs& a, const uint16_t* q, 
   }
 }
 
+// a / b of two counts, most of which fit 32 bits (a 64-bit division is long).
+__device__ __forceinline__ int64_t div_run(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // Sum over the block of one value per thread, and the sum of the threads
 // before this one.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sh, int64_t* total) {
@@ -423,14 +428,15 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
   pdl_trigger();
 
   // ---- where this CTA's run of tiles starts
-  int64_t total;
+  int64_t total, all, run;
   {
     const int per = (a.nq + kGqaThreads - 1) / kGqaThreads;
     const int i0 = min(tid * per, a.nq), i1 = min(i0 + per, a.nq);
     int64_t n = 0;
     for (int i = i0; i < i1; ++i) n += tile_range<kRows>(__ldg(a.query_pos + i), a.window, a.n_sink).count;
     int64_t start = block_scan(n, scan_s, &total);
-    const int64_t all = total * a.groups, run = (all + a.n_cta - 1) / a.n_cta;
+    all = total * a.groups;
+    run = div_run(all + a.n_cta - 1, a.n_cta);
     const int64_t u = (int64_t)blockIdx.x * run;
     if (blockIdx.x == 0 || (start * a.groups <= u && u < (start + n) * a.groups)) {
       for (int i = i0; i < i1; ++i) {
@@ -443,11 +449,10 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
         start += c;
       }
     }
-    if (blockIdx.x == 0 && tid == 0) a.starts[a.nq] = total;
+    if (blockIdx.x == 0 && tid == 0) a.starts[a.nq] = run;
     __syncthreads();
     if (u >= all) return;
   }
-  const int64_t all = total * a.groups, run = (all + a.n_cta - 1) / a.n_cta;
   const int64_t u_begin = (int64_t)blockIdx.x * run, u_end = min(u_begin + run, all);
   const int Hq = a.Hkv * a.G;
 
@@ -461,7 +466,7 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
       ++qi;
       continue;
     }
-    const int grp = (int)((u - q_start) / ur.count);
+    const int grp = a.groups == 1 ? 0 : (int)div_run(u - q_start, ur.count);
     const int64_t i_start = q_start + (int64_t)grp * ur.count, i_end = i_start + ur.count;
     const int32_t c0 = (int32_t)(u - i_start), c1 = (int32_t)(min(u_end, i_end) - i_start);
     const int32_t seq = a.seq_of_query ? __ldg(a.seq_of_query + qi) : qi;
@@ -615,76 +620,121 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
 }
 
 // Joins the parts of every item that several CTAs share, and writes the
-// outputs of queries that see no row.  One block per (query, virtual head).
-constexpr int kCombThreads = 128;
-constexpr int kCombWarps = kCombThreads / 32;
-template <int D>
-__global__ void __launch_bounds__(kCombThreads) gqa_combine_kernel(const __grid_constant__ GqaArgs a, int32_t run_heads) {
-  __shared__ float acc_s[kCombWarps][D];
+// outputs of queries that see no row.  W warps work on one query head of one
+// query: the parts' weights first, then their rows, eight of a warp's in
+// flight.  Latency is all there is to it (a serial walk over 128 parts took
+// 24 us): eight warps per row where there are few rows, one where there are
+// many, whose parts are few.
+constexpr int kMaxCtas = 2 * 160;      // main-kernel CTAs at most: the workspace is sized without a device
+constexpr int kCombWarps = 8;
+template <int D, int W>
+__global__ void __launch_bounds__(kCombWarps * 32) gqa_combine_kernel(const __grid_constant__ GqaArgs a,
+                                                                      int32_t run_heads) {
+  constexpr int R = kCombWarps / W;                    // rows per block
+  constexpr int V = D / 32;                            // values per lane
+  __shared__ float acc_s[W > 1 ? W : 1][D];
+  __shared__ float w_s[R][kMaxCtas];
   __shared__ float m_s[kCombWarps], l_s[kCombWarps];
-  const int r = blockIdx.x, qi = blockIdx.y;           // query head, query
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int32_t pos = __ldg(a.query_pos + qi);
-  const int32_t count = tile_range<kRows>(pos, a.window, a.n_sink).count;
-  const int64_t at = (int64_t)qi * (a.Hkv * a.G) + r;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wr = warp % W, rr = warp / W;
+  const int Hq = a.Hkv * a.G;
+  const int64_t at = (int64_t)blockIdx.x * R + rr;     // row of the output
+  const bool live = at < (int64_t)a.nq * Hq;
+  const int qi = live ? (int)(at / Hq) : 0, r = live ? (int)(at % Hq) : 0;
+  const int32_t count = tile_range<kRows>(__ldg(a.query_pos + qi), a.window, a.n_sink).count;
+  const int vh = (r / a.G) * a.subs + (r % a.G) / run_heads, grp = vh / a.per_cta;
   pdl_wait();
+  if (!live) return;
   if (count == 0) {
-    for (int i = threadIdx.x; i < D / 2; i += kCombThreads) reinterpret_cast<uint32_t*>(a.out + at * D)[i] = 0u;
-    if (threadIdx.x == 0 && a.lse) a.lse[at] = -INFINITY;
+    for (int i = wr * 32 + lane; i < D / 2; i += W * 32) reinterpret_cast<uint32_t*>(a.out + at * D)[i] = 0u;
+    if (wr == 0 && lane == 0 && a.lse) a.lse[at] = -INFINITY;
     return;
   }
-  const int vh = (r / a.G) * a.subs + (r % a.G) / run_heads, grp = vh / a.per_cta;
-  const int64_t all = __ldcg(a.starts + a.nq) * a.groups, run = (all + a.n_cta - 1) / a.n_cta;
-  const int64_t i0 = __ldcg(a.starts + qi) * a.groups + (int64_t)grp * count, i1 = i0 + count;
-  const int64_t first = i0 / run, last = (i1 - 1) / run;
-  if (first == last) return;                           // one CTA had the whole item
+  const int64_t run = __ldcg(a.starts + a.nq);
+  const int64_t i0 = __ldcg(a.starts + qi) * a.groups + (int64_t)grp * count;
+  const int first = (int)div_run(i0, run), parts = (int)div_run(i0 + count - 1, run) - first + 1;
+  if (parts == 1) return;                              // one CTA had the whole item
   const int rows = a.per_cta * run_heads, row = (vh - grp * a.per_cta) * run_heads + (r % a.G) % run_heads;
-  auto part = [&](int64_t c) { return (2 * c + (c == first ? 1 : 0)) * rows + row; };
+  // part p: the first CTA's last part, then each CTA's first
+  auto part = [&](int p) { return (int64_t)(2 * (first + p) + (p == 0 ? 1 : 0)) * rows + row; };
+  auto block_sync = [&]() {
+    if (W > 1) __syncthreads();                        // W == kCombWarps: the block is one row
+    else __syncwarp();
+  };
   float M = -INFINITY;
-  for (int64_t c = first + threadIdx.x; c <= last; c += kCombThreads) M = fmaxf(M, __ldcg(&a.part_ml[part(c)]).x);
+  for (int p = wr * 32 + lane; p < parts; p += W * 32) M = fmaxf(M, __ldcg(&a.part_ml[part(p)]).x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) m_s[warp] = M;
-  __syncthreads();
+  if (W > 1) {
+    if (lane == 0) m_s[warp] = M;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kCombWarps; ++w) M = fmaxf(M, m_s[w]);
-  constexpr int V = D / 32;                            // values per lane
-  float acc[V], l = 0.f;
+    for (int w = 0; w < W; ++w) M = fmaxf(M, m_s[w]);
+  }
+  float l = 0.f;
+  for (int p = wr * 32 + lane; p < parts; p += W * 32) {
+    const float2 ml = __ldcg(&a.part_ml[part(p)]);
+    // a part without a maximum saw only NaN, and its sum says so
+    const float f = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - M);
+    w_s[rr][p] = f;
+    l += f * ml.y;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (W > 1 && lane == 0) l_s[warp] = l;
+  block_sync();
+  float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll 4
-  for (int64_t c = first + warp; c <= last; c += kCombWarps) {
-    const int64_t p = part(c);
-    const float2 ml = __ldcg(&a.part_ml[p]);
-    const float f = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - M);
-    const float* o = a.part_o + p * D + lane * V;
-    l += f * ml.y;
-    if constexpr (V == 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(o));
-      acc[0] += f * v.x, acc[1] += f * v.y, acc[2] += f * v.z, acc[3] += f * v.w;
-    } else {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(o));
-      acc[0] += f * v.x, acc[1] += f * v.y;
+  for (int p0 = wr; p0 < parts; p0 += 8 * W) {
+    float o[8][V];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int p = p0 + i * W;
+      const float* src = a.part_o + part(p) * D + lane * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[i][e] = 0.f;
+      if (p < parts) {
+        if constexpr (V == 4) {
+          const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+          o[i][0] = v.x, o[i][1] = v.y, o[i][2] = v.z, o[i][3] = v.w;
+        } else {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+          o[i][0] = v.x, o[i][1] = v.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int p = p0 + i * W;
+      const float f = p < parts ? w_s[rr][p] : 0.f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] += f * o[i][e];
     }
   }
+  if (W > 1) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc_s[warp][lane * V + i] = acc[i];
-  if (lane == 0) l_s[warp] = l;
-  __syncthreads();
-  l = 0.f;
+    for (int i = 0; i < V; ++i) acc_s[wr][lane * V + i] = acc[i];
+    __syncthreads();
+    if (wr > 0) return;
+    l = 0.f;
 #pragma unroll
-  for (int w = 0; w < kCombWarps; ++w) l += l_s[w];
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  for (int i = threadIdx.x; i < D; i += kCombThreads) {
-    float v = 0.f;
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
 #pragma unroll
-    for (int w = 0; w < kCombWarps; ++w) v += acc_s[w][i];
-    reinterpret_cast<__nv_bfloat16*>(a.out)[at * D + i] = __float2bfloat16_rn(v * inv);
+    for (int w = 0; w < W; ++w) {
+      l += l_s[w];
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += acc_s[w][lane * V + i];
+    }
   }
-  if (threadIdx.x == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * D) + lane * (V / 2);
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+    dst[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  if (lane == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
 }
-
-constexpr int kMaxCtas = 2 * 160;      // main-kernel CTAs at most: the workspace is sized without a device
 
 template <int D, int NT>
 cudaError_t launch_gqa_t(GqaArgs& a, cudaStream_t st) {
@@ -698,8 +748,12 @@ cudaError_t launch_gqa_t(GqaArgs& a, cudaStream_t st) {
   gqa_split_kernel<D, NT><<<a.n_cta, kGqaThreads, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_k(gqa_combine_kernel<D>, dim3(a.Hkv * a.G, a.nq), dim3(kCombThreads), 0, st, false, true, a,
-                  (int32_t)(8 * NT));
+  const int64_t rows = (int64_t)a.nq * a.Hkv * a.G;
+  if (rows <= 4 * sm_count())
+    return launch_k(gqa_combine_kernel<D, kCombWarps>, dim3((unsigned)rows), dim3(kCombWarps * 32), 0, st, false, true, a,
+                    (int32_t)(8 * NT));
+  return launch_k(gqa_combine_kernel<D, 1>, dim3((unsigned)((rows + kCombWarps - 1) / kCombWarps)),
+                  dim3(kCombWarps * 32), 0, st, false, true, a, (int32_t)(8 * NT));
 }
 
 // How query heads map to warps: runs of 8 NT heads of a KV head, up to 8 runs per CTA.

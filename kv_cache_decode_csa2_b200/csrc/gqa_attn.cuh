@@ -37,7 +37,7 @@ struct GqaArgs {
   int32_t subs;                    // runs per KV head
   int32_t per_cta;                 // virtual heads per CTA
   int32_t groups;                  // CTA groups per query: ceil(vh / per_cta)
-  int64_t* starts;                 // [nq + 1] tiles of one group before each query; the total
+  int64_t* starts;                 // [nq + 1] tiles of one group before each query; tiles per CTA
   float* part_o;                   // [2 n_cta][rows][D] unnormalised O of a part
   float2* part_ml;                 // [2 n_cta][rows] (offset max in log2 units, sum)
   int32_t* status;
