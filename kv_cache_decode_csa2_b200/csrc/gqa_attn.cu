@@ -33,10 +33,8 @@ namespace csa2 {
 namespace {
 
 constexpr int kGqaThreads = 256;
+constexpr int kMaxCtas = 2 * 160;     // main-kernel CTAs at most: the workspace is sized without a device
 constexpr int kGqaWarps = kGqaThreads / 32;
-constexpr float kLazy = 5.f;          // how far a logit may exceed the maximum in use (log2)
-constexpr float kOffset = 10.f;       // weights are 2^(s - m + kOffset)
-
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -49,34 +47,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-// Eight codes to four f16 pairs, in order.  The bytes are taken apart by name
-// (mov.b32), which the conversion reads in place: 81 values per clock and SM
-// with the multiply by the scale, against 43 with shifts and masks.
-__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&o)[4]) {
-  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-      "mov.b32 {a, b, c, d}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // A warp's ring of tiles in shared memory.  A tile is kRows rows of one KV
 // head: K codes as they are (a lane reads its quarter row), V codes of every 16
 // rows with rows 0, 2, 4, 6 next to one another, then 1, 3, 5, 7 and so on (the
@@ -107,28 +77,6 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-// The page of row p in a plane (0 where it is contiguous, -1 past the table).
-__device__ __forceinline__ int32_t page_of(const RowMap& m, int32_t shift, int32_t p) {
-  return shift >= 0 ? p >> shift : p / m.page_rows;
-}
-__device__ __forceinline__ int32_t load_page(const RowMap& m, int32_t shift, int32_t seq, int32_t p) {
-  if (!m.page_table) return 0;
-  const int32_t pg = page_of(m, shift, p);
-  return seq < 0 || pg >= m.max_pages ? -1 : __ldg(m.page_table + (int64_t)seq * m.max_pages + pg);
-}
-// Physical row of position p (a multiple of kPageStep), of whose step the
-// rows up to position `last` are wanted; -1 when they are not all in the plane.
-__device__ __forceinline__ int64_t step_base(const RowMap& m, int32_t shift, int32_t seq, int32_t p, int32_t page,
-                                             int32_t last) {
-  const int32_t n = min(kPageStep - 1, last - p);
-  int64_t r;
-  if (m.page_table)
-    r = page < 0 ? -1 : (int64_t)page * m.page_rows + (p - page_of(m, shift, p) * m.page_rows);
-  else
-    r = seq < 0 || (m.seq_rows > 0 && p + n >= m.seq_rows) ? -1 : (int64_t)seq * m.seq_rows + p;
-  return r >= 0 && r + n < m.n_rows ? r : -1;
-}
 
 // Where a lane's parts of the tiles come from: it copies 16 bytes of every
 // 32 / kPer-th row of K and of V, and loads the scales of row `lane` of both.
@@ -377,11 +325,6 @@ __device__ __forceinline__ void load_query(const GqaArgs& a, const uint16_t* q, 
   }
 }
 
-// a / b of two counts, most of which fit 32 bits (a 64-bit division is long).
-__device__ __forceinline__ int64_t div_run(int64_t a, int64_t b) {
-  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
-}
-
 // Sum over the block of one value per thread, and the sum of the threads
 // before this one.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sh, int64_t* total) {
@@ -449,7 +392,7 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
         start += c;
       }
     }
-    if (blockIdx.x == 0 && tid == 0) a.starts[a.nq] = run;
+    if (blockIdx.x == 0 && tid == 0) a.starts[a.nq] = total, a.starts[a.nq + 1] = run;
     __syncthreads();
     if (u >= all) return;
   }
@@ -625,7 +568,6 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
 // flight.  Latency is all there is to it (a serial walk over 128 parts took
 // 24 us): eight warps per row where there are few rows, one where there are
 // many, whose parts are few.
-constexpr int kMaxCtas = 2 * 160;      // main-kernel CTAs at most: the workspace is sized without a device
 constexpr int kCombWarps = 8;
 template <int D, int W>
 __global__ void __launch_bounds__(kCombWarps * 32) gqa_combine_kernel(const __grid_constant__ GqaArgs a,
@@ -640,20 +582,23 @@ __global__ void __launch_bounds__(kCombWarps * 32) gqa_combine_kernel(const __gr
   const int64_t at = (int64_t)blockIdx.x * R + rr;     // row of the output
   const bool live = at < (int64_t)a.nq * Hq;
   const int qi = live ? (int)(at / Hq) : 0, r = live ? (int)(at % Hq) : 0;
-  const int32_t count = tile_range<kRows>(__ldg(a.query_pos + qi), a.window, a.n_sink).count;
   const int vh = (r / a.G) * a.subs + (r % a.G) / run_heads, grp = vh / a.per_cta;
+  const int block = a.q_tile > 0 ? qi / a.q_tile : qi, n_block = a.q_tile > 0 ? (a.nq + a.q_tile - 1) / a.q_tile : a.nq;
   pdl_wait();
   if (!live) return;
+  const int64_t before = __ldcg(a.starts + block), run = __ldcg(a.starts + n_block + 1);
+  const int64_t count = __ldcg(a.starts + block + 1) - before;
   if (count == 0) {
     for (int i = wr * 32 + lane; i < D / 2; i += W * 32) reinterpret_cast<uint32_t*>(a.out + at * D)[i] = 0u;
     if (wr == 0 && lane == 0 && a.lse) a.lse[at] = -INFINITY;
     return;
   }
-  const int64_t run = __ldcg(a.starts + a.nq);
-  const int64_t i0 = __ldcg(a.starts + qi) * a.groups + (int64_t)grp * count;
+  const int64_t i0 = before * a.groups + grp * count;
   const int first = (int)div_run(i0, run), parts = (int)div_run(i0 + count - 1, run) - first + 1;
   if (parts == 1) return;                              // one CTA had the whole item
-  const int rows = a.per_cta * run_heads, row = (vh - grp * a.per_cta) * run_heads + (r % a.G) % run_heads;
+  const int rows = a.q_tile > 0 ? kBlockRows : a.per_cta * run_heads;
+  const int row = a.q_tile > 0 ? (qi % a.q_tile) * min(run_heads, a.G - (vh % a.subs) * run_heads) + (r % a.G) % run_heads
+                               : (vh - grp * a.per_cta) * run_heads + (r % a.G) % run_heads;
   // part p: the first CTA's last part, then each CTA's first
   auto part = [&](int p) { return (int64_t)(2 * (first + p) + (p == 0 ? 1 : 0)) * rows + row; };
   auto block_sync = [&]() {
@@ -748,12 +693,7 @@ cudaError_t launch_gqa_t(GqaArgs& a, cudaStream_t st) {
   gqa_split_kernel<D, NT><<<a.n_cta, kGqaThreads, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int64_t rows = (int64_t)a.nq * a.Hkv * a.G;
-  if (rows <= 4 * sm_count())
-    return launch_k(gqa_combine_kernel<D, kCombWarps>, dim3((unsigned)rows), dim3(kCombWarps * 32), 0, st, false, true, a,
-                    (int32_t)(8 * NT));
-  return launch_k(gqa_combine_kernel<D, 1>, dim3((unsigned)((rows + kCombWarps - 1) / kCombWarps)),
-                  dim3(kCombWarps * 32), 0, st, false, true, a, (int32_t)(8 * NT));
+  return launch_gqa_combine(a, D, 8 * NT, st);
 }
 
 // How query heads map to warps: runs of 8 NT heads of a KV head, up to 8 runs per CTA.
@@ -769,32 +709,53 @@ void gqa_heads(GqaArgs& a, int32_t Hkv, int32_t G, int* nt) {
 
 void carve_gqa(GqaArgs& a, Carver& c, int32_t nq, int32_t D, int nt) {
   const size_t parts = 2 * (size_t)kMaxCtas * a.per_cta * 8 * nt;
-  a.starts = c.take<int64_t>((size_t)nq + 1);
+  a.starts = c.take<int64_t>((size_t)nq + 2);
+  a.part_o = c.take<float>(parts * D);
+  a.part_ml = c.take<float2>(parts);
+}
+
+// The block kernel's parts: one CTA per SM, kBlockRows rows each.
+void carve_block(GqaArgs& a, Carver& c, int32_t nq, int32_t D) {
+  const size_t parts = (size_t)kMaxCtas * kBlockRows;
+  a.starts = c.take<int64_t>((size_t)nq + 2);
   a.part_o = c.take<float>(parts * D);
   a.part_ml = c.take<float2>(parts);
 }
 
 }  // namespace
 
+cudaError_t launch_gqa_combine(const GqaArgs& a, int32_t D, int32_t run_heads, cudaStream_t st) {
+  const int64_t rows = (int64_t)a.nq * a.Hkv * a.G;
+  const bool few = rows <= 4 * sm_count();
+  const dim3 grid((unsigned)(few ? rows : (rows + kCombWarps - 1) / kCombWarps)), block(kCombWarps * 32);
+  if (D == 128)
+    return few ? launch_k(gqa_combine_kernel<128, kCombWarps>, grid, block, 0, st, false, true, a, run_heads)
+               : launch_k(gqa_combine_kernel<128, 1>, grid, block, 0, st, false, true, a, run_heads);
+  return few ? launch_k(gqa_combine_kernel<64, kCombWarps>, grid, block, 0, st, false, true, a, run_heads)
+             : launch_k(gqa_combine_kernel<64, 1>, grid, block, 0, st, false, true, a, run_heads);
+}
+
 size_t gqa_scratch_bytes(int32_t nq, int32_t Hq, int32_t Hkv, int32_t D) {
   GqaArgs a{};
   int nt;
   gqa_heads(a, Hkv, Hq / Hkv, &nt);
-  Carver c(nullptr);
+  Carver c(nullptr), b(nullptr);
   carve_gqa(a, c, nq, D, nt);
-  return c.used + 256;
+  carve_block(a, b, nq, D);
+  return (c.used > b.used ? c.used : b.used) + 256;
 }
 
 cudaError_t launch_gqa_attn(const uint16_t* q, const csa2_kv_cache& kv, const int32_t* seq_of_query,
                             const int32_t* query_pos, int32_t nq, int32_t Hq, int32_t window, int32_t n_sink,
                             float scale, bool group_queries, uint16_t* out, float* lse, void* ws, int32_t* status,
                             cudaStream_t st) {
-  (void)group_queries;
   GqaArgs a{};
   int nt;
+  const bool blocks = group_queries && nq > 1;
   gqa_heads(a, kv.Hkv, Hq / kv.Hkv, &nt);
   Carver c(ws);
-  carve_gqa(a, c, nq, kv.D, nt);
+  if (blocks) carve_block(a, c, nq, kv.D);
+  else carve_gqa(a, c, nq, kv.D, nt);
   a.q = q, a.out = out, a.lse = lse;
   const csa2_rows* views[4] = {&kv.k_codes, &kv.k_scales, &kv.v_codes, &kv.v_scales};
   a.one_map = 1;
@@ -814,6 +775,10 @@ cudaError_t launch_gqa_attn(const uint16_t* q, const csa2_kv_cache& kv, const in
   a.n_sink = window > 0 ? n_sink : 0;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.status = status;
+  if (blocks) {
+    gqa_block_shape(a);
+    return launch_gqa_block(a, kv.D, st);
+  }
   if (kv.D == 128) return nt == 1 ? launch_gqa_t<128, 1>(a, st) : launch_gqa_t<128, 2>(a, st);
   return nt == 1 ? launch_gqa_t<64, 1>(a, st) : launch_gqa_t<64, 2>(a, st);
 }

@@ -13,6 +13,7 @@
 #pragma once
 
 #include "csa2_device.cuh"
+#include "fp4_device.cuh"
 #include "internal.h"
 
 namespace csa2 {
@@ -33,11 +34,12 @@ struct GqaArgs {
   int32_t nq, Hkv, G, window, n_sink;
   float scale_log2;
   int32_t n_cta;                   // CTAs of the main kernel
+  int32_t q_tile;                  // queries per item of the block kernel (0: the split kernel, one query per item)
   int32_t vh;                      // virtual heads: (KV head, run of up to 8 NT query heads)
   int32_t subs;                    // runs per KV head
   int32_t per_cta;                 // virtual heads per CTA
-  int32_t groups;                  // CTA groups per query: ceil(vh / per_cta)
-  int64_t* starts;                 // [nq + 1] tiles of one group before each query; tiles per CTA
+  int32_t groups;                  // items per query or block: ceil(vh / per_cta)
+  int64_t* starts;                 // tiles of one group before each query or block, their number, tiles per CTA
   float* part_o;                   // [2 n_cta][rows][D] unnormalised O of a part
   float2* part_ml;                 // [2 n_cta][rows] (offset max in log2 units, sum)
   int32_t* status;
@@ -70,5 +72,71 @@ struct Seen {
 __device__ __forceinline__ Seen seen_rows(int32_t pos, int32_t window, int32_t n_sink) {
   return Seen{pos, window > 0 && pos >= window ? pos - window + 1 : 0, n_sink};
 }
+
+constexpr float kLazy = 5.f;          // how far a logit may exceed the maximum in use (log2)
+constexpr float kOffset = 10.f;       // weights are 2^(s - m + kOffset)
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Eight codes to four f16 pairs, in order.  The bytes are taken apart by name
+// (mov.b32), which the conversion reads in place: 81 values per clock and SM
+// with the multiply by the scale, against 43 with shifts and masks.
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// The page of row p in a plane (0 where it is contiguous, -1 past the table).
+__device__ __forceinline__ int32_t page_of(const RowMap& m, int32_t shift, int32_t p) {
+  return shift >= 0 ? p >> shift : p / m.page_rows;
+}
+__device__ __forceinline__ int32_t load_page(const RowMap& m, int32_t shift, int32_t seq, int32_t p) {
+  if (!m.page_table) return 0;
+  const int32_t pg = page_of(m, shift, p);
+  return seq < 0 || pg >= m.max_pages ? -1 : __ldg(m.page_table + (int64_t)seq * m.max_pages + pg);
+}
+// Physical row of position p (a multiple of kPageStep), of whose step the
+// rows up to position `last` are wanted; -1 when they are not all in the plane.
+__device__ __forceinline__ int64_t step_base(const RowMap& m, int32_t shift, int32_t seq, int32_t p, int32_t page,
+                                             int32_t last) {
+  const int32_t n = min(kPageStep - 1, last - p);
+  int64_t r;
+  if (m.page_table)
+    r = page < 0 ? -1 : (int64_t)page * m.page_rows + (p - page_of(m, shift, p) * m.page_rows);
+  else
+    r = seq < 0 || (m.seq_rows > 0 && p + n >= m.seq_rows) ? -1 : (int64_t)seq * m.seq_rows + p;
+  return r >= 0 && r + n < m.n_rows ? r : -1;
+}
+
+// a / b of two counts, most of which fit 32 bits (a 64-bit division is long).
+__device__ __forceinline__ int64_t div_run(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
+// Joins the parts that CTAs left (gqa_attn.cu); launched behind either kernel.
+cudaError_t launch_gqa_combine(const GqaArgs& a, int32_t D, int32_t run_heads, cudaStream_t st);
+// Blocks of queries on the tensor cores (gqa_block.cu): the fields of a that
+// describe the work, the CTAs at most and the rows of a part; the launch.
+constexpr int kBlockRows = 256;    // query rows of an item: two MMA heights
+void gqa_block_shape(GqaArgs& a);
+cudaError_t launch_gqa_block(GqaArgs& a, int32_t D, cudaStream_t st);
 
 }  // namespace csa2
