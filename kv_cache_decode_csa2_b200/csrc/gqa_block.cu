@@ -7,13 +7,18 @@
 //   S_m [128 rows][128 positions] = Q_m K^T      (tcgen05, f16 -> fp32 in TMEM)
 //   P_m = exp2(S_m scale - max + offset)          (f16, over S_m's columns)
 //   O_m [128 rows][D] += P_m V                   (A operand from TMEM)
-// One persistent CTA per SM, 17 warps:
+// One persistent CTA per SM, 16 warps (17 would cost every thread 32 of its
+// 128 registers):
 //   warps 0-7   softmax, four per height, a thread per row: the running maximum
 //               (lazy, as in the split kernel) and sum, P to TMEM, O at the end
-//   warps 8-15  expand the codes of K and V into f16 tiles in shared memory
+//   warps 8-14  expand the codes of K and V into f16 tiles in shared memory
 //               (code x scale is exact), two stages each
-//   warp 16     issues the MMAs, and builds the next item's list of runs
-// While one height's softmax works, the tensor cores take the other's products.
+//   warp 15     issues the MMAs, and lists the runs of the next item
+// The issuer takes the heights in turn (P V of a tile, then Q K^T of the next),
+// so that the tensor cores work for one while the other is at its softmax;
+// issued by the softmax warps themselves the heights fell into step, and an
+// issuing warp was late for its own tile.  An item of at most 128 rows has its
+// tiles dealt out to the two heights in turn, whose results join at the end.
 // The queries of a block may belong to several sequences: each run of queries
 // of one sequence walks its own tiles, and the others' rows are masked there.
 //
@@ -28,9 +33,10 @@ namespace csa2 {
 namespace {
 
 constexpr int kT = 128;                          // cache rows per tile
-constexpr int kSoftWarps = 8, kFillWarps = 8;
+constexpr int kSoftWarps = 8, kFillWarps = 7;
 constexpr int kIssueWarp = kSoftWarps + kFillWarps;
-constexpr int kBlockThreads = 32 * (kIssueWarp + 1);
+constexpr int kWarps = kIssueWarp + 1;
+constexpr int kBlockThreads = 32 * kWarps;
 constexpr int kMaxRuns = 256;                    // runs of a block, at most one per query
 constexpr int kCountWarps = 7;                   // warps that count tiles in the prologue (their scratch is shared memory)
 constexpr int kBadRing = 4;
@@ -60,10 +66,35 @@ struct BlockSmem {
 };
 
 struct Bars {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], item_full[2], item_empty[2], q_full,
-      o_full, drain;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], item_full[2], item_empty[2],
+      q_full, both_done, stored, taken, drain;
 };
 
+// Waits as mbar_wait does, but asleep for up to a few microseconds at a time:
+// sixteen warps that poll take the issue slots of those that work.
+__device__ __forceinline__ bool sleepy_try(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(4000u)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool block_wait(uint64_t* bar, uint32_t parity, volatile int32_t* abort_flag) {
+  if (sleepy_try(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (true) {
+    if (sleepy_try(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
 // MN-major operand tile with the 128-byte swizzle: 64 values along MN are 128
 // contiguous bytes, 8 steps along K follow at 128 bytes; `mn` bytes lead to the
 // next 64 values and 1024 to the next 8 steps.  Fields as smem_desc_kmajor.
@@ -86,6 +117,27 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
       : "memory");
 }
+// A tcgen05.ld delivers its registers only at the wait: the values go through
+// it, so that nothing that uses them can be placed before.
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
+  uint32_t (&lo)[16] = *reinterpret_cast<uint32_t (*)[16]>(&r[0]);
+  uint32_t (&hi)[16] = *reinterpret_cast<uint32_t (*)[16]>(&r[16]);
+  tmem_wait_ld16(lo);
+  tmem_wait_ld16(hi);
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
@@ -93,6 +145,28 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15]), "r"(taddr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
+               : "memory");
+}
+// Two fp32 operations per instruction.
+__device__ __forceinline__ float2 fma2(uint32_t x0, uint32_t x1, float m, float c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\tmov.b64 z, {%5, %5};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "r"(x0), "r"(x1), "f"(m), "f"(c));
+  return r;
+}
+__device__ __forceinline__ void add2(float2& acc, float x0, float x1) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(acc.x), "+f"(acc.y)
+      : "f"(x0), "f"(x1));
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -157,28 +231,24 @@ __device__ int32_t list_runs(const GqaArgs& a, int32_t q0, int32_t n, Runs& r, i
 // A role's walk over the tiles of an item.
 struct Walk {
   const Item& it;
-  const GqaArgs& a;
-  int32_t run, first, end;                       // run at hand and its tiles
-  __device__ __forceinline__ Walk(const Item& i, const GqaArgs& args) : it(i), a(args), run(-1), first(0), end(0) {}
+  int32_t n_sink, run, first, end;               // run at hand and its tiles
+  int32_t seq, hi, lo, qa, qb;                   // what it is: sequence, rows, queries [qa, qb) of the block
+  TileRange t;
+  __device__ __forceinline__ Walk(const Item& i, const GqaArgs& a) : it(i), n_sink(a.n_sink), run(-1), first(0), end(0) {}
   // Row of tile x (x does not fall from call to call).
   __device__ __forceinline__ int32_t row(int32_t x) {
-    while (x >= end) {
-      ++run;
-      first = it.cum[run];
-      end = it.cum[run + 1];
+    if (x >= end) {
+      do {
+        ++run;
+        first = it.cum[run];
+        end = it.cum[run + 1];
+      } while (x >= end);
+      seq = it.runs.seq[run], hi = it.runs.hi[run], lo = it.runs.lo[run];
+      qa = it.runs.q[run], qb = it.runs.q[run + 1];
+      t = run_tiles(hi, lo, n_sink);
     }
-    return run_tiles(it.runs.hi[run], it.runs.lo[run], a.n_sink).row(x - first, kT);
+    return t.row(x - first, kT);
   }
-};
-
-// One lane's parts of a tile in the fill: a block of 32 codes of K and of V in
-// one or two rows, with all the row's scales.
-template <int D>
-struct Fill {
-  static constexpr int kPass = D / 64;           // passes over the tile: 64 rows each, or all 128
-  uint4 k[kPass], v[kPass];
-  uint32_t ks[kPass], vs[kPass];
-  uint32_t bad;                                  // bit s: step s of the tile is not there
 };
 
 template <int D>
@@ -191,7 +261,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::bars + 32 * 8);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
   int32_t* bad_s = reinterpret_cast<int32_t*>(tmem_slot + 4);          // [kBadRing][2]
-  __shared__ int64_t scan_s[kIssueWarp + 1];
+  __shared__ int64_t scan_s[kWarps];
+  __shared__ float2 join_s[128];
   __shared__ int32_t first_s;
   __shared__ int64_t first_start_s;
   static_assert(sizeof(Bars) <= 32 * 8, "barriers");
@@ -207,24 +278,28 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       mbar_init(&bar->v_full[i], kFillWarps);
       mbar_init(&bar->v_empty[i], 1);
       mbar_init(&bar->s_full[i], 1);
-      mbar_init(&bar->p_full[i], 4);
+      mbar_init(&bar->p_full[i], 4);             // the four warps of a height
+      mbar_init(&bar->o_full[i], 1);
       mbar_init(&bar->item_full[i], 1);
       mbar_init(&bar->item_empty[i], kSoftWarps + kFillWarps);
     }
+    mbar_init(&bar->both_done, kSoftWarps);      // both heights of an item that they share
+    mbar_init(&bar->stored, 4);
+    mbar_init(&bar->taken, 4);
     mbar_init(&bar->q_full, kSoftWarps);
-    mbar_init(&bar->o_full, 1);
     mbar_init(&bar->drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == kIssueWarp) {
+  if (warp == 0) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   int32_t* counts = reinterpret_cast<int32_t*>(sm + kCountWarps * sizeof(Runs));
-  if (warp < kCountWarps) {
-    Runs& scratch = reinterpret_cast<Runs*>(sm)[warp];
-    for (int b = warp; b < n_blocks; b += kCountWarps) {
+  if (warp >= kWarps - kCountWarps) {
+    const int cw = warp - (kWarps - kCountWarps);
+    Runs& scratch = reinterpret_cast<Runs*>(sm)[cw];
+    for (int b = cw; b < n_blocks; b += kCountWarps) {
       int32_t n_runs;
       const int32_t c = list_runs(a, b * a.q_tile, min(a.q_tile, a.nq - b * a.q_tile), scratch, nullptr, &n_runs);
       if (lane == 0) counts[b] = c;
@@ -250,7 +325,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
     if (lane == 31) scan_s[warp] = s;
     __syncthreads();
     int64_t total = 0, start = s - n;
-    for (int w = 0; w <= kIssueWarp; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       if (w < warp) start += scan_s[w];
       total += scan_s[w];
     }
@@ -312,67 +387,82 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       __syncwarp();
     };
     constexpr uint32_t kIdS = idesc_f16(128, kT, 0), kIdO = idesc_f16(128, D, 1);
-    const uint32_t q_s = smem_u32(sm + L::q), k_s = smem_u32(sm + L::k), v_s = smem_u32(sm + L::v);
-    auto logits = [&](int m, int st) {           // S_m = Q_m K^T
+    const uint64_t q_d = smem_desc_kmajor(smem_u32(sm + L::q), 128), k_d = smem_desc_kmajor(smem_u32(sm + L::k), 128),
+                   v_d = smem_desc_mnmajor(smem_u32(sm + L::v), kT * 128);
+    auto wait = [&](uint64_t* b, uint32_t parity) {
+      return (bool)__all_sync(0xffffffffu, block_wait(b, parity, abort_flag));
+    };
+    // Issued by one elected lane; descriptors come from uniform registers.
+    auto logits = [&](int m, uint32_t n) {       // S_m = Q_m K^T of the CTA's tile n
+      const uint64_t qd = q_d + (uint32_t)(m * (L::kPlane >> 4)), kd = k_d + (uint32_t)((n & 1) * (L::kPlane >> 4));
 #pragma unroll
       for (int i = 0; i < D / 16; ++i) {
-        const uint32_t off = (i / 4) * (kT * 128) + (i % 4) * 32;
-        mma_ss(tmem + m * kT, smem_desc_kmajor(q_s + m * L::kPlane + off, 128), smem_desc_kmajor(k_s + st * L::kPlane + off, 128),
-               kIdS, i > 0);
+        const uint32_t off = ((i / 4) * (kT * 128) + (i % 4) * 32) >> 4;
+        mma_ss(tmem + m * kT, qd + off, kd + off, kIdS, i > 0);
       }
       mma_commit(&bar->s_full[m]);
     };
+    auto values = [&](int m, uint32_t n, bool first) {   // O_m += P_m V of tile n
+      const uint64_t vd = v_d + (uint32_t)((n & 1) * (L::kPlane >> 4));
+#pragma unroll
+      for (int i = 0; i < kT / 16; ++i)
+        mma_ts(tmem + 256 + m * D, tmem + m * kT + i * 8, vd + (uint32_t)(i * (2048 >> 4)), kIdO, !first || i > 0);
+    };
     build(0);
     if (lane == 0) mbar_arrive(&bar->item_full[0]);
-    uint32_t n = 0, tiles_m[2] = {0, 0};         // tiles so far, of all and of each height
+    uint32_t n0 = 0, n_p[2] = {0, 0};            // tiles before the item; batches of each height
     for (uint32_t i = 0;; ++i) {
       const Item& it = items[i & 1];
       if (it.q0 < 0) break;
-      const int heights = it.n_q * it.gs > 128 ? 2 : 1, tiles = it.c1 - it.c0;
-      bool ok = true;
-      if (lane == 0) {
-        ok = mbar_wait(&bar->q_full, i & 1, abort_flag) && mbar_wait(&bar->k_full[n & 1], (n >> 1) & 1, abort_flag);
-        if (ok) {
-          tc_fence_after();
-          for (int m = 0; m < heights; ++m) logits(m, n & 1);
-          mma_commit(&bar->k_empty[n & 1]);
+      const bool pair = it.n_q * it.gs <= 128;   // both heights hold the same rows and take every other tile
+      const uint32_t tiles = it.c1 - it.c0;
+      bool ok = wait(&bar->q_full, i & 1) && wait(&bar->k_full[n0 & 1], (n0 >> 1) & 1);
+      if (ok && pair && tiles > 1) ok = wait(&bar->k_full[(n0 + 1) & 1], ((n0 + 1) >> 1) & 1);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
+        logits(0, n0);
+        if (!pair) logits(1, n0);
+        mma_commit(&bar->k_empty[n0 & 1]);
+        if (pair && tiles > 1) {
+          logits(1, n0 + 1);
+          mma_commit(&bar->k_empty[(n0 + 1) & 1]);
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
+      __syncwarp();
       // the next item, while the first tile's softmax works
-      ok = i < 1 || mbar_wait(&bar->item_empty[(i + 1) & 1], ((i - 1) >> 1) & 1, abort_flag);
-      if (!__all_sync(0xffffffffu, ok)) break;
+      if (i > 0 && !wait(&bar->item_empty[(i + 1) & 1], ((i - 1) >> 1) & 1)) break;
       build((i + 1) & 1);
-      if (lane == 0) {
-        mbar_arrive(&bar->item_full[(i + 1) & 1]);
-        for (int j = 0; j < tiles && ok; ++j, ++n) {
-          const int st = n & 1;
-          ok = mbar_wait(&bar->v_full[st], (n >> 1) & 1, abort_flag);
-          for (int m = 0; m < heights && ok; ++m) {
-            ok = mbar_wait(&bar->p_full[m], tiles_m[m]++ & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            for (int x = 0; x < kT / 16; ++x)
-              mma_ts(tmem + 256 + m * D, tmem + m * kT + x * 8, smem_desc_mnmajor(v_s + st * L::kPlane + x * 2048, kT * 128),
-                     kIdO, j > 0 || x > 0);
-            if (j + 1 < tiles) {
-              if (m == 0) ok = mbar_wait(&bar->k_full[st ^ 1], ((n + 1) >> 1) & 1, abort_flag);
-              if (!ok) break;
-              tc_fence_after();
-              logits(m, st ^ 1);
-            }
+      if (lane == 0) mbar_arrive(&bar->item_full[(i + 1) & 1]);
+      // batches: P V of a tile, then Q K^T of the height's next.  The operands
+      // are waited for before P: while an S product reads shared memory at its
+      // full rate, a barrier there takes hundreds of clocks.
+      const uint32_t step = pair ? 2 : 1, batches = pair ? tiles : 2 * tiles;
+      for (uint32_t b = 0; b < batches && ok; ++b) {
+        const int m = b & 1;
+        const uint32_t j = pair ? b : b >> 1, n = n0 + j, nn = n + step;
+        const bool more = j + step < tiles, last_use = pair || m == 1;
+        ok = wait(&bar->v_full[n & 1], (n >> 1) & 1) && (!more || wait(&bar->k_full[nn & 1], (nn >> 1) & 1)) &&
+             wait(&bar->p_full[m], n_p[m] & 1);
+        if (!ok) break;
+        ++n_p[m];
+        tc_fence_after();
+        if (elect_one()) {
+          values(m, n, j < step);
+          if (last_use) mma_commit(&bar->v_empty[n & 1]);
+          if (more) {
+            logits(m, nn);
+            if (last_use) mma_commit(&bar->k_empty[nn & 1]);
+          } else {
+            mma_commit(&bar->o_full[m]);
           }
-          if (!ok) break;
-          mma_commit(&bar->v_empty[st]);
-          if (j + 1 < tiles) mma_commit(&bar->k_empty[st ^ 1]);
         }
-        if (ok) mma_commit(&bar->o_full);
+        __syncwarp();
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
+      n0 += tiles;
     }
-    if (lane == 0) {                             // nothing may still read shared memory when the CTA ends
+    if (elect_one()) {                           // nothing may still read shared memory when the CTA ends
       mma_commit(&bar->drain);
       const uint64_t t0 = global_ns();
       while (!mbar_try_wait(&bar->drain, 0) && global_ns() - t0 < 100000000ull) {
@@ -381,114 +471,185 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
     __syncwarp();
   } else if (warp >= kSoftWarps) {
     // ================================================== fill: codes to f16 tiles
+    // A group is 8 (D = 64: 16) rows of a tile, a lane a block of 32 codes of one of
+    // them; lanes are laid out so that a quarter of a warp stores to all 32
+    // banks.  Warp f expands groups f, f + 7, ... of K and 6 - f, 13 - f, ... of V.
     const int fw = warp - kSoftWarps;
-    constexpr int P = Fill<D>::kPass;
-    // lanes are laid out so that a quarter of a warp stores to all 32 banks
-    const int row = D == 128 ? fw * 8 + ((lane >> 1) & 3) + (lane >> 4) * 4 : fw * 16 + (lane >> 1);
+    constexpr int NG = D == 128 ? 16 : 8, PER = (NG + kFillWarps - 1) / kFillWarps, GR = kT / NG;
+    const int in_g = D == 128 ? ((lane >> 1) & 3) + (lane >> 4) * 4 : lane >> 1;
     const int blk32 = D == 128 ? (lane & 1) + ((lane >> 3) & 1) * 2 : lane & 1;
+    const int vw = kFillWarps - 1 - fw;
+    // Offsets of this lane's rows within a step of each plane.  Everything that
+    // does not change from tile to tile is here: with the addresses worked out
+    // per tile, the fill was longer than the softmax.
+    uint32_t ko[PER], kso[PER], kno[PER], vo[PER], vso[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const uint32_t rk = ((fw + j * kFillWarps) * GR + in_g) & (kPageStep - 1);
+      const uint32_t rv = ((vw + j * kFillWarps) * GR + in_g) & (kPageStep - 1);
+      ko[j] = rk * (uint32_t)a.rb[0] + blk32 * 16;
+      kso[j] = rk * (uint32_t)a.rb[1];
+      kno[j] = rk * (uint32_t)a.rb[3];
+      vo[j] = rv * (uint32_t)a.rb[2] + blk32 * 16;
+      vso[j] = rv * (uint32_t)a.rb[3];
+    }
     uint32_t n = 0;
     for (uint32_t i = 0;; ++i) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&bar->item_full[i & 1], (i >> 1) & 1, abort_flag))) break;
+      if (!__all_sync(0xffffffffu, block_wait(&bar->item_full[i & 1], (i >> 1) & 1, abort_flag))) break;
       const Item& it = items[i & 1];
       if (it.q0 < 0) break;
-      Walk walk(it, a);
-      const int head = it.head;
-      auto load = [&](int32_t x, Fill<D>& f) {
-        const int32_t p0 = walk.row(x), seq = it.runs.seq[walk.run], hi = it.runs.hi[walk.run];
-        const Seen seen = Seen{hi, it.runs.lo[walk.run], a.n_sink}.from(p0);
-        f.bad = 0;
+      const uint8_t* const bk = a.base[0] + it.head * (D / 2);
+      const uint8_t* const bks = a.base[1] + it.head * (D / 32);
+      const uint8_t* const bv = a.base[2] + it.head * (D / 2);
+      const uint8_t* const bvs = a.base[3] + it.head * (D / 32);
+      // pages of the two steps of a tile, looked up a tile ahead (they cost a
+      // trip to memory before the rows can be asked for)
+      Walk scout(it, a), walk(it, a);
+      int32_t page[2][4];
+      // where the head's codes and scales of each step's first row are
+      const uint8_t *k0, *k1, *v0, *v1, *ks0, *ks1, *vs0, *vs1;
+      bool there[2];                             // the step has rows to see, and they are in the planes
+      int32_t bad = 0;                           // bit s: step s of the tile is not there
+      Seen seen{-1, 0, 0};
+      auto wanted = [&](const Seen& w, int s) {  // a step without a row to see may have no page
+        return s * kPageStep <= w.hi && ((s + 1) * kPageStep > w.lo || s * kPageStep < w.sk);
+      };
+      auto look_up = [&](int32_t x) {
+        const int32_t p0 = scout.row(x);
+        const Seen w = Seen{scout.hi, scout.lo, a.n_sink}.from(p0);
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-          const int rr = p * 64 + row, step = D == 128 ? p : fw >> 2;    // row of the tile, its step
-          const int32_t sp = p0 + step * kPageStep;
-          f.k[p] = f.v[p] = make_uint4(0, 0, 0, 0);
-          f.ks[p] = f.vs[p] = 0;
-          const int32_t s0 = step * kPageStep;
-          // a step without a row to see may have no page
-          if (!(s0 <= seen.hi && (s0 + kPageStep > seen.lo || s0 < seen.sk))) continue;
-          int64_t r[4];
+        for (int s = 0; s < 2; ++s) {
+          if (!wanted(w, s)) continue;
+          page[s][0] = load_page(a.map[0], a.page_shift[0], scout.seq, p0 + s * kPageStep);
+          if (!a.one_map)
+#pragma unroll
+            for (int y = 1; y < 4; ++y) page[s][y] = load_page(a.map[y], a.page_shift[y], scout.seq, p0 + s * kPageStep);
+        }
+      };
+      auto rows_of = [&](int32_t x) {            // moves to tile x
+        const int32_t p0 = walk.row(x);
+        seen = Seen{walk.hi, walk.lo, a.n_sink}.from(p0);
+        bad = 0;
+        auto place = [&](int s, const uint8_t*& k, const uint8_t*& ks, const uint8_t*& v, const uint8_t*& vs) {
+          there[s] = false;
+          if (!wanted(seen, s)) return;
+          uint32_t r[4];                         // rows of a plane fit 31 bits
           bool ok = true;
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            r[y] = y > 0 && a.one_map ? r[0]
-                                      : step_base(a.map[y], a.page_shift[y], seq, sp, load_page(a.map[y], a.page_shift[y], seq, sp), hi);
-            ok = ok && r[y] >= 0;
+            if (y == 0 || !a.one_map) {
+              const int64_t b = step_base(a.map[y], a.page_shift[y], walk.seq, p0 + s * kPageStep, page[s][y], walk.hi);
+              ok = ok && b >= 0;
+              r[y] = (uint32_t)b;
+            } else {
+              r[y] = r[0];
+            }
           }
-          if (!ok) {
-            f.bad |= 1u << step;
-            continue;
-          }
-          if (!seen.row(rr)) continue;
-          const int in = rr - s0;
-          f.k[p] = __ldg(reinterpret_cast<const uint4*>(a.base[0] + (r[0] + in) * a.rb[0] + head * (D / 2) + blk32 * 16));
-          f.v[p] = __ldg(reinterpret_cast<const uint4*>(a.base[2] + (r[2] + in) * a.rb[2] + head * (D / 2) + blk32 * 16));
-          const uint8_t* ks = a.base[1] + (r[1] + in) * a.rb[1] + head * (D / 32);
-          const uint8_t* vs = a.base[3] + (r[3] + in) * a.rb[3] + head * (D / 32);
-          if (D == 128) {
-            f.ks[p] = __ldg(reinterpret_cast<const uint32_t*>(ks));
-            f.vs[p] = __ldg(reinterpret_cast<const uint32_t*>(vs));
-          } else {
-            f.ks[p] = __ldg(reinterpret_cast<const uint16_t*>(ks));
-            f.vs[p] = __ldg(reinterpret_cast<const uint16_t*>(vs));
+          there[s] = ok;
+          if (!ok) bad |= 1 << s;
+          k = bk + (uint64_t)r[0] * (uint32_t)a.rb[0];
+          ks = bks + (uint64_t)r[1] * (uint32_t)a.rb[1];
+          v = bv + (uint64_t)r[2] * (uint32_t)a.rb[2];
+          vs = bvs + (uint64_t)r[3] * (uint32_t)a.rb[3];
+        };
+        place(0, k0, ks0, v0, vs0);
+        place(1, k1, ks1, v1, vs1);
+        if (bad && fw == 0 && lane == 0) record_error(a.status, CSA2_ERR_INDEX_RANGE);
+        if (x + 1 < it.c1) look_up(x + 1);
+      };
+      uint4 kc[PER], vc[PER];
+      uint32_t ks[PER], kn[PER], vs[PER];        // scales of the K rows, of their V rows, of the V rows
+      auto load_scales = [&](const uint8_t* p) {
+        return D == 128 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p));
+      };
+      auto mine = [&](int g) {                   // whether this lane's row of group g is to be read
+        return g < NG && (g >= NG / 2 ? there[1] : there[0]) && seen.row(g * GR + in_g);
+      };
+      auto load_k = [&]() {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          const int g = fw + j * kFillWarps;
+          const bool s = g >= NG / 2;
+          kc[j] = make_uint4(0, 0, 0, 0);
+          ks[j] = kn[j] = 0;
+          if (mine(g)) {
+            kc[j] = __ldg(reinterpret_cast<const uint4*>((s ? k1 : k0) + ko[j]));
+            ks[j] = load_scales((s ? ks1 : ks0) + kso[j]);
+            kn[j] = load_scales((s ? vs1 : vs0) + kno[j]);
           }
         }
-        if (f.bad && lane == 0) record_error(a.status, CSA2_ERR_INDEX_RANGE);
       };
-      // 32 codes of row rr times their scale to the f16 tile
-      auto expand = [&](uint8_t* plane, int rr, const uint4& c, uint32_t scale) {
+      auto load_v = [&]() {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          const int g = vw + j * kFillWarps;
+          const bool s = g >= NG / 2;
+          vc[j] = make_uint4(0, 0, 0, 0);
+          vs[j] = 0;
+          if (mine(g)) {
+            vc[j] = __ldg(reinterpret_cast<const uint4*>((s ? v1 : v0) + vo[j]));
+            vs[j] = load_scales((s ? vs1 : vs0) + vso[j]);
+          }
+        }
+      };
+      // 32 codes of a row of group g times their scale to the f16 tile
+      auto expand = [&](uint8_t* plane, int g, const uint4& c, uint32_t scale) {
         const uint32_t s2 = e4m3x2_to_f16x2(scale * 0x101u);
         const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-        uint8_t* base = plane + (blk32 >> 1) * (kT * 128) + rr * 128;
+        const int rr = g * GR + in_g;
+        uint8_t* at = plane + (blk32 >> 1) * (kT * 128) + rr * 128;
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           uint32_t o[4];
           e2m1x8_to_f16(w[y], o);
-          *reinterpret_cast<uint4*>(base + ((((blk32 & 1) * 4 + y) ^ (rr & 7)) << 4)) =
+          *reinterpret_cast<uint4*>(at + ((((blk32 & 1) * 4 + y) ^ (rr & 7)) << 4)) =
               make_uint4(mul_f16x2(o[0], s2), mul_f16x2(o[1], s2), mul_f16x2(o[2], s2), mul_f16x2(o[3], s2));
         }
       };
-      Fill<D> f[2];
-      load(it.c0, f[0]);
+      look_up(it.c0);
+      rows_of(it.c0);
+      load_k();
+      load_v();
       bool ok = true;
-      for (int32_t x = it.c0; x < it.c1 && ok;) {
+      for (int32_t x = it.c0; x < it.c1; ++x, ++n) {
+        const int st = n & 1;
+        const uint32_t par = ((n >> 1) & 1) ^ 1;
+        ok = __all_sync(0xffffffffu, block_wait(&bar->k_empty[st], par, abort_flag));
+        if (!ok) break;
+        if (fw == 0 && lane == 0) bad_s[(n % kBadRing) * 2] = bad & 1, bad_s[(n % kBadRing) * 2 + 1] = bad >> 1;
 #pragma unroll
-        for (int b = 0; b < 2; ++b, ++x, ++n) {
-          if (x >= it.c1 || !ok) break;
-          if (x + 1 < it.c1) load(x + 1, f[b ^ 1]);
-          const Fill<D>& c = f[b];
-          const int st = n & 1;
-          const uint32_t par = ((n >> 1) & 1) ^ 1;
-          ok = __all_sync(0xffffffffu, mbar_wait(&bar->k_empty[st], par, abort_flag));
-          if (!ok) break;
-          if (lane == 0 && (D == 128 ? fw == 0 : (fw & 3) == 0)) {
-            if (D == 128) bad_s[(n % kBadRing) * 2] = c.bad & 1, bad_s[(n % kBadRing) * 2 + 1] = c.bad >> 1;
-            else bad_s[(n % kBadRing) * 2 + (fw >> 2)] = c.bad != 0;
-          }
+        for (int j = 0; j < PER; ++j) {
+          const int g = fw + j * kFillWarps;
+          if (g >= NG) break;
+          // any NaN scale among the row's values: the row's logits are NaN
+          uint32_t s = (ks[j] >> (8 * blk32)) & 0xFFu;
+          bool nan = false;
 #pragma unroll
-          for (int p = 0; p < P; ++p) {
-            // any NaN scale among the row's values: the row's logits are NaN
-            uint32_t s = (c.ks[p] >> (8 * blk32)) & 0xFFu;
-            bool nan = false;
-#pragma unroll
-            for (int y = 0; y < D / 32; ++y) nan |= ((c.vs[p] >> (8 * y)) & 0x7Fu) == 0x7Fu;
-            if (nan) s = 0x7Fu;
-            expand(sm + L::k + st * L::kPlane, p * 64 + row, c.k[p], s);
-          }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar->k_full[st]);
-          ok = __all_sync(0xffffffffu, mbar_wait(&bar->v_empty[st], par, abort_flag));
-          if (!ok) break;
-#pragma unroll
-          for (int p = 0; p < P; ++p) {
-            uint32_t s = (c.vs[p] >> (8 * blk32)) & 0xFFu;
-            if ((s & 0x7Fu) == 0x7Fu) s = 0;
-            expand(sm + L::v + st * L::kPlane, p * 64 + row, c.v[p], s);
-          }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar->v_full[st]);
+          for (int y = 0; y < D / 32; ++y) nan |= ((kn[j] >> (8 * y)) & 0x7Fu) == 0x7Fu;
+          if (nan) s = 0x7Fu;
+          expand(sm + L::k + st * L::kPlane, g, kc[j], s);
         }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->k_full[st]);
+        if (x + 1 < it.c1) {
+          rows_of(x + 1);
+          load_k();
+        }
+        ok = __all_sync(0xffffffffu, block_wait(&bar->v_empty[st], par, abort_flag));
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          const int g = vw + j * kFillWarps;
+          if (g >= NG) break;
+          uint32_t s = (vs[j] >> (8 * blk32)) & 0xFFu;
+          if ((s & 0x7Fu) == 0x7Fu) s = 0;
+          expand(sm + L::v + st * L::kPlane, g, vc[j], s);
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->v_full[st]);
+        if (x + 1 < it.c1) load_v();
       }
       if (!ok) break;
       __syncwarp();
@@ -499,15 +660,18 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
     const int m = warp >> 2, r = tid & 127;      // height, row of it
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t s_t = tmem + m * kT + lanes, o_t = tmem + 256 + m * D + lanes;
-    uint32_t n_all = 0, n_s = 0;                 // tiles so far, and those of this height
+    uint32_t n_all = 0, n_s = 0, n_o = 0, n_pair = 0;   // tiles so far, of all and of this height; outputs; shared items
     for (uint32_t i = 0;; ++i) {
-      if (!__all_sync(0xffffffffu, mbar_wait(&bar->item_full[i & 1], (i >> 1) & 1, abort_flag))) break;
+      if (!__all_sync(0xffffffffu, block_wait(&bar->item_full[i & 1], (i >> 1) & 1, abort_flag))) break;
       const Item& it = items[i & 1];
       if (it.q0 < 0) break;
-      const int rows = it.n_q * it.gs, at = m * 128 + r;
+      const int rows = it.n_q * it.gs;
+      const bool pair = rows <= 128;             // both heights hold the same rows and take every other tile
+      const int at = (pair ? 0 : m * 128) + r, step = pair ? 2 : 1;
       const bool live = at < rows;
       const int qr = live ? at / it.gs : 0;      // query of the block
       const int64_t out_row = (int64_t)(it.q0 + qr) * Hq + it.head * a.G + it.r0 + (at - qr * it.gs);
+      const int32_t x0 = it.c0 + (pair ? m : 0), c1 = it.c1;
       // ---- this row of Q, scaled by a power of two into f16
       float qs;
       {
@@ -540,121 +704,173 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       tc_fence_before();                         // O of the item before has been read
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->q_full);
+      bool ok = true;
       const int32_t pos = live ? __ldg(a.query_pos + it.q0 + qr) : -1;
       const Seen mine = seen_rows(pos, a.window, a.n_sink);
-      float mo = -INFINITY, l = 0.f;
-      bool ok = true;
-      const bool active = m == 0 || rows > 128;
+      float mo = -INFINITY;
+      float2 l = make_float2(0.f, 0.f);
       Walk walk(it, a);
-      for (int32_t x = it.c0; x < it.c1 && active; ++x, ++n_s) {
+      for (int32_t x = x0; x < c1; x += step, ++n_s) {
         const int32_t p0 = walk.row(x);
         // what this row sees of the tile: everything, or by a mask
-        const bool in_run = pos >= 0 && qr >= it.runs.q[walk.run] && qr < it.runs.q[walk.run + 1];
+        const bool in_run = pos >= 0 && qr >= walk.qa && qr < walk.qb;
         const Seen w = mine.from(p0);
-        ok = __all_sync(0xffffffffu, mbar_wait(&bar->s_full[m], n_s & 1, abort_flag));
+        const uint32_t t = n_all + (uint32_t)(x - it.c0);
+        ok = __all_sync(0xffffffffu, ok && block_wait(&bar->s_full[m], n_s & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
-        const uint32_t t = n_all + (uint32_t)(x - it.c0);
         const int32_t bad0 = bad_s[(t % kBadRing) * 2], bad1 = bad_s[(t % kBadRing) * 2 + 1];
         const bool full = __all_sync(0xffffffffu, in_run && w.all(kT) && !(bad0 | bad1));
-        uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-        if (!full) {
-          // bits of columns [32 y, 32 y + 32): c <= hi && (c >= lo || c < sk)
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            auto below = [&](int32_t c) {        // columns < c
-              const int32_t k = c - 32 * y;
-              return k <= 0 ? 0u : (k >= 32 ? ~0u : (1u << k) - 1u);
-            };
-            see[y] = below(w.hi + 1) & (~below(w.lo) | below(w.sk));
-            if (!in_run || (y < 2 ? bad0 : bad1)) see[y] = 0;
-          }
-        }
-        // the largest logit seen
-        float top = -INFINITY;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
+        // bits of columns [32 y, 32 y + 32) seen: c <= hi && (c >= lo || c < sk)
+        auto below = [](int32_t k) { return k <= 0 ? 0u : (k >= 32 ? ~0u : (1u << k) - 1u); };
+        auto see = [&](int y) {
+          if (!in_run || (y < 2 ? bad0 : bad1)) return 0u;
+          return below(w.hi + 1 - 32 * y) & (~below(w.lo - 32 * y) | below(w.sk - 32 * y));
+        };
+        // The weights, 32 columns at a time, over the logits' columns.  The
+        // maximum moves only when a logit exceeds it by kLazy: O, the sum and
+        // the weights of the tile already stored are then scaled, and these
+        // columns, taken on trust, are taken again.  (One rolled loop: the
+        // code of the roles has to stay in the instruction caches together.)
+#pragma unroll 1
+        for (int y = 0; y < 4;) {
           uint32_t s[32];
           tmem_ld32(s_t + 32 * y, s);
-          tmem_wait_ld();
-          if (full) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) top = fmaxf(top, __uint_as_float(s[c]));
-          } else {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) top = (see[y] >> c) & 1u ? fmaxf(top, __uint_as_float(s[c])) : top;
-          }
-        }
-        top = top == -INFINITY ? top : top * qs;
-        if (__any_sync(0xffffffffu, top > mo + (kOffset + kLazy))) {
-          const float m_new = fmaxf(mo, top - kOffset);
-          const float f = mo == -INFINITY ? 0.f : ex2(mo - m_new);
-          mo = m_new;
-          l *= f;
-          if (x > it.c0) {
-#pragma unroll 1
-            for (int y = 0; y < D / 32; ++y) {
-              uint32_t o[32];
-              tmem_ld32(o_t + 32 * y, o);
-              tmem_wait_ld();
-              uint32_t half[16];
-#pragma unroll
-              for (int z = 0; z < 2; ++z) {
-#pragma unroll
-                for (int c = 0; c < 16; ++c) half[c] = __float_as_uint(__uint_as_float(o[16 * z + c]) * f);
-                tmem_st16(o_t + 32 * y + 16 * z, half);
-              }
-            }
-            tmem_wait_st();
-          }
-        }
-        // the weights, over the logits' columns
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t s[32], p[16];
-          tmem_ld32(s_t + 32 * y, s);
-          tmem_wait_ld();
-          if (full) {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) s[c] = __float_as_uint(ex2(fmaf(__uint_as_float(s[c]), qs, -mo)));
-          } else {
+          tmem_wait_ld32(s);
+          if (!full) {
+            const uint32_t bits = see(y);        // unseen: a logit of -inf, whatever it was
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              s[c] = (see[y] >> c) & 1u ? __float_as_uint(ex2(fmaf(__uint_as_float(s[c]), qs, -mo))) : 0u;
+              if (!((bits >> c) & 1u)) s[c] = 0xFF800000u;
           }
+          const float sub = mo == -INFINITY ? 0.f : mo;
+          float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const float p0f = __uint_as_float(s[2 * c]), p1f = __uint_as_float(s[2 * c + 1]);
-            l += p0f + p1f;
+            const float2 v = fma2(s[2 * c], s[2 * c + 1], qs, -sub);
+            s[2 * c] = __float_as_uint(v.x), s[2 * c + 1] = __float_as_uint(v.y);
+            top[c & 1] = fmaxf(top[c & 1], fmaxf(v.x, v.y));
+          }
+          float2 add = make_float2(0.f, 0.f);
+          uint32_t p[16];
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float p0f = ex2(__uint_as_float(s[2 * c])), p1f = ex2(__uint_as_float(s[2 * c + 1]));
+            add2(add, p0f, p1f);
             const __half2 hh = __floats2half2_rn(p0f, p1f);
             p[c] = *reinterpret_cast<const uint32_t*>(&hh);
           }
-          tmem_st16(s_t + 16 * y, p);
+          const float most = fmaxf(top[0], top[1]);
+          if (!__any_sync(0xffffffffu, most > (mo == -INFINITY ? -INFINITY : kOffset + kLazy))) {
+            l.x += add.x, l.y += add.y;
+            tmem_st16(s_t + 16 * y, p);
+            ++y;
+            continue;
+          }
+          // a whole number: weights already rounded are scaled exactly
+          const float m_new = fmaxf(mo, floorf(most + sub) - kOffset);
+          const float f = mo == -INFINITY ? 0.f : ex2(mo - m_new);
+          mo = m_new;
+          l.x *= f, l.y *= f;
+          tmem_wait_st();                        // the weights before are in place
+#pragma unroll 1
+          for (int z = 0; z < 2 * y; ++z) {
+            uint32_t b[8];
+            tmem_ld8(s_t + 8 * z, b);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {        // in fp32: f may be below f16's smallest step
+              const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&b[c]));
+              const __half2 hh = __floats2half2_rn(v.x * f, v.y * f);
+              b[c] = *reinterpret_cast<const uint32_t*>(&hh);
+            }
+            tmem_st8(s_t + 8 * z, b);
+          }
+          if (x > x0) {
+#pragma unroll 1
+            for (int z = 0; z < D / 8; ++z) {
+              uint32_t o[8];
+              tmem_ld8(o_t + 8 * z, o);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+              tmem_st8(o_t + 8 * z, o);
+            }
+          }
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->p_full[m]);
       }
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      n_all += (uint32_t)(it.c1 - it.c0);
+      const bool some = x0 < c1;
+      if (some) {
+        ok = __all_sync(0xffffffffu, block_wait(&bar->o_full[m], n_o++ & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      n_all += (uint32_t)(c1 - it.c0);
+      float sum = l.x + l.y, scale = 1.f;
+      if (pair) {
+        // the second height's maximum, sum and O join the first's, in the space of Q
+        float* o_s = reinterpret_cast<float*>(sm + L::q);      // [D / 4][128 rows] of four values
+        if (lane == 0) mbar_arrive(&bar->both_done);           // and its products are done with it
+        ok = __all_sync(0xffffffffu, block_wait(&bar->both_done, n_pair & 1, abort_flag));
+        if (!ok) break;
+        if (m == 1) {
+#pragma unroll 1
+          for (int y = 0; y < D / 16; ++y) {
+            uint32_t o[16];
+            if (some) {
+              tmem_ld16(o_t + 16 * y, o);
+              tmem_wait_ld16(o);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              reinterpret_cast<uint4*>(o_s)[(4 * y + c) * 128 + r] =
+                  some ? make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]) : make_uint4(0, 0, 0, 0);
+          }
+          join_s[r] = make_float2(mo, sum);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->stored);
+        } else {
+          ok = __all_sync(0xffffffffu, block_wait(&bar->stored, n_pair & 1, abort_flag));
+          if (!ok) break;
+          const float2 ml = join_s[r];
+          const float top = fmaxf(mo, ml.x);
+          // a side without a maximum saw nothing, or only NaN: its sum is 0 or NaN
+          const float f0 = mo == -INFINITY ? (sum != sum ? sum : 0.f) : ex2(mo - top);
+          scale = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - top);
+          sum = sum * f0 + ml.y * scale;
+          mo = top;
+          l.x = f0;                              // O of the first height is scaled by it below
+        }
+      }
       // ---- the output, or this CTA's part of it
-      ok = __all_sync(0xffffffffu, mbar_wait(&bar->o_full, i & 1, abort_flag));
-      if (!ok) break;
-      tc_fence_after();
-      if (active) {
+      if (!pair || m == 0) {
         const int slot = it.slot;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const int64_t part = (int64_t)slot * kBlockRows + at;
 #pragma unroll 1
-        for (int y = 0; y < D / 32; ++y) {
-          uint32_t o[32];
-          tmem_ld32(o_t + 32 * y, o);
-          tmem_wait_ld();
-          if (live && slot < 0) {
-            uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D + 32 * y);
+        for (int y = 0; y < D / 16; ++y) {
+          uint32_t o[16];
+          tmem_ld16(o_t + 16 * y, o);
+          tmem_wait_ld16(o);
+          if (pair) {
+            const uint4* other = reinterpret_cast<const uint4*>(sm + L::q);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
+              const uint4 b = other[(4 * y + c) * 128 + r];
+              const uint32_t bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                o[4 * c + e] = __float_as_uint(__uint_as_float(o[4 * c + e]) * l.x + __uint_as_float(bw[e]) * scale);
+            }
+          }
+          if (live && slot < 0) {
+            uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * D + 16 * y);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
               uint32_t b[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -665,22 +881,28 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
               dst[c] = make_uint4(b[0], b[1], b[2], b[3]);
             }
           } else if (live) {
-            uint4* dst = reinterpret_cast<uint4*>(a.part_o + part * D + 32 * y);
+            uint4* dst = reinterpret_cast<uint4*>(a.part_o + part * D + 16 * y);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
+            for (int c = 0; c < 4; ++c) dst[c] = make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]);
           }
         }
         if (live && slot < 0 && a.lse)
-          a.lse[out_row] = l == 0.f ? -INFINITY : (mo + log2f(l)) * 0.69314718055994531f;
-        if (live && slot >= 0) a.part_ml[part] = make_float2(mo, l);
+          a.lse[out_row] = sum == 0.f ? -INFINITY : (mo + log2f(sum)) * 0.69314718055994531f;
+        if (live && slot >= 0) a.part_ml[part] = make_float2(mo, sum);
       }
       __syncwarp();
+      if (pair) {                                // the space of Q is free when the first height has read it
+        if (m == 0 && lane == 0) mbar_arrive(&bar->taken);
+        ok = __all_sync(0xffffffffu, block_wait(&bar->taken, n_pair & 1, abort_flag));
+        if (!ok) break;
+        ++n_pair;
+      }
       if (lane == 0) mbar_arrive(&bar->item_empty[i & 1]);
     }
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == kIssueWarp) {
+  if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
