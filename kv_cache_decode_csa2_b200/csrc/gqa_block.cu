@@ -13,7 +13,7 @@
 //               (lazy, as in the split kernel) and sum, P to TMEM, O at the end
 //   warps 8-14  expand the codes of K and V into f16 tiles in shared memory
 //               (code x scale is exact), two stages each
-//   warp 15     issues the MMAs, and lists the runs of the next item
+//   warp 15     issues the MMAs, and works out ahead where the others' tiles are
 // The issuer takes the heights in turn (P V of a tile, then Q K^T of the next),
 // so that the tensor cores work for one while the other is at its softmax;
 // issued by the softmax warps themselves the heights fell into step, and an
@@ -39,7 +39,16 @@ constexpr int kWarps = kIssueWarp + 1;
 constexpr int kBlockThreads = 32 * kWarps;
 constexpr int kMaxRuns = 256;                    // runs of a block, at most one per query
 constexpr int kCountWarps = 7;                   // warps that count tiles in the prologue (their scratch is shared memory)
-constexpr int kBadRing = 4;
+constexpr int kBatch = 16;                       // tiles whose places are worked out together
+
+// Where a tile is: worked out kBatch tiles at a time, a lane per step of 64
+// rows (done by every filling warp for itself, it took longer than the softmax).
+struct alignas(16) Place {
+  Seen seen;                                     // its rows that any query of the run sees
+  int32_t flags;                                 // bit s: step s is there; bit 2 + s: it should be and is not; bit 4: all rows
+  uint32_t r[2][4];                              // first physical row of each step in each plane
+  int32_t row, qa, qb, pad;                      // its first row; the run's queries [qa, qb) of the block
+};
 
 // The runs of a block: consecutive queries of one sequence.
 struct Runs {
@@ -61,13 +70,14 @@ template <int D>
 struct BlockSmem {
   static constexpr int kPlane = kT * D * 2;      // an f16 tile: [D / 64][128 rows][128 bytes], 128B swizzle
   static constexpr int q = 0, k = 2 * kPlane, v = k + 2 * kPlane, items = v + 2 * kPlane;
-  static constexpr int bars = items + 2 * (int)sizeof(Item);
+  static constexpr int places = (items + 2 * (int)sizeof(Item) + 15) / 16 * 16;
+  static constexpr int bars = places + 2 * kBatch * (int)sizeof(Place);
   static constexpr int total = bars + 32 * 8 + 64;
 };
 
 struct Bars {
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_full[2], item_full[2], item_empty[2],
-      q_full, both_done, stored, taken, drain;
+      place_full[2], q_full, both_done, stored, taken, drain;
 };
 
 // Waits as mbar_wait does, but asleep for up to a few microseconds at a time:
@@ -228,29 +238,6 @@ __device__ int32_t list_runs(const GqaArgs& a, int32_t q0, int32_t n, Runs& r, i
   return total;
 }
 
-// A role's walk over the tiles of an item.
-struct Walk {
-  const Item& it;
-  int32_t n_sink, run, first, end;               // run at hand and its tiles
-  int32_t seq, hi, lo, qa, qb;                   // what it is: sequence, rows, queries [qa, qb) of the block
-  TileRange t;
-  __device__ __forceinline__ Walk(const Item& i, const GqaArgs& a) : it(i), n_sink(a.n_sink), run(-1), first(0), end(0) {}
-  // Row of tile x (x does not fall from call to call).
-  __device__ __forceinline__ int32_t row(int32_t x) {
-    if (x >= end) {
-      do {
-        ++run;
-        first = it.cum[run];
-        end = it.cum[run + 1];
-      } while (x >= end);
-      seq = it.runs.seq[run], hi = it.runs.hi[run], lo = it.runs.lo[run];
-      qa = it.runs.q[run], qb = it.runs.q[run + 1];
-      t = run_tiles(hi, lo, n_sink);
-    }
-    return t.row(x - first, kT);
-  }
-};
-
 template <int D>
 __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __grid_constant__ GqaArgs a) {
   using L = BlockSmem<D>;
@@ -260,7 +247,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
   Bars* bar = reinterpret_cast<Bars*>(sm + L::bars);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::bars + 32 * 8);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(tmem_slot + 1);
-  int32_t* bad_s = reinterpret_cast<int32_t*>(tmem_slot + 4);          // [kBadRing][2]
+  Place* places = reinterpret_cast<Place*>(sm + L::places);            // [2][kBatch]
   __shared__ int64_t scan_s[kWarps];
   __shared__ float2 join_s[128];
   __shared__ int32_t first_s;
@@ -281,6 +268,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       mbar_init(&bar->p_full[i], 4);             // the four warps of a height
       mbar_init(&bar->o_full[i], 1);
       mbar_init(&bar->item_full[i], 1);
+      mbar_init(&bar->place_full[i], 1);
       mbar_init(&bar->item_empty[i], kSoftWarps + kFillWarps);
     }
     mbar_init(&bar->both_done, kSoftWarps);      // both heights of an item that they share
@@ -408,8 +396,62 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       for (int i = 0; i < kT / 16; ++i)
         mma_ts(tmem + 256 + m * D, tmem + m * kT + i * 8, vd + (uint32_t)(i * (2048 >> 4)), kIdO, !first || i > 0);
     };
+    // Works out the places of kBatch tiles of an item from tile x on, into half
+    // `h` of the ring: lane 2 k + s has step s of tile x + k.
+    auto locate = [&](const Item& it, int32_t x, uint32_t h) {
+      const int32_t t = x + (lane >> 1);
+      const int s = lane & 1;
+      const bool in = t < it.c1;
+      Place* pl = places + h * kBatch + (lane >> 1);
+      bool ok = false, bad = false;
+      int k = 0;
+      int32_t p0 = 0;
+      Seen w{-1, 0, 0};
+      if (in) {
+        int hi = it.n_runs - 1;                  // the run with cum <= t < cum of the next
+        while (k < hi) {
+          const int mid = (k + hi + 1) >> 1;
+          if (it.cum[mid] <= t) k = mid;
+          else hi = mid - 1;
+        }
+        const int32_t last = it.runs.hi[k], seq = it.runs.seq[k];
+        p0 = run_tiles(last, it.runs.lo[k], a.n_sink).row(t - it.cum[k], kT);
+        w = Seen{last, it.runs.lo[k], a.n_sink}.from(p0);
+        // a step without a row to see may have no page
+        if (s * kPageStep <= w.hi && ((s + 1) * kPageStep > w.lo || s * kPageStep < w.sk)) {
+          const int32_t at = p0 + s * kPageStep;
+          uint32_t r0 = 0;
+          ok = true;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            if (y == 0 || !a.one_map) {
+              const int64_t b = step_base(a.map[y], a.page_shift[y], seq, at, load_page(a.map[y], a.page_shift[y], seq, at), last);
+              ok = ok && b >= 0;
+              r0 = (uint32_t)b;                  // rows of a plane fit 31 bits
+            }
+            pl->r[s][y] = r0;
+          }
+          bad = !ok;
+        }
+      }
+      __syncwarp();
+      int32_t flags = (ok ? 1 << s : 0) | (bad ? 4 << s : 0);
+      flags |= __shfl_xor_sync(0xffffffffu, flags, 1);
+      if (in && s == 0) {
+        pl->seen = w;
+        pl->flags = flags | ((flags & 3) == 3 && w.all(kT) ? 16 : 0);
+        pl->row = p0;
+        pl->qa = it.runs.q[k];
+        pl->qb = it.runs.q[k + 1];
+      }
+      if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(a.status, CSA2_ERR_INDEX_RANGE);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->place_full[h]);
+    };
     build(0);
     if (lane == 0) mbar_arrive(&bar->item_full[0]);
+    uint32_t batch = 0;                          // batches of places so far
+    if (items[0].q0 >= 0) locate(items[0], items[0].c0, 0);
     uint32_t n0 = 0, n_p[2] = {0, 0};            // tiles before the item; batches of each height
     for (uint32_t i = 0;; ++i) {
       const Item& it = items[i & 1];
@@ -458,6 +500,14 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
           }
         }
         __syncwarp();
+        // The first tile of a batch is through: the batch before is done with
+        // (its tiles' P have all been taken), and its half of the ring is free.
+        if (j % kBatch == 0 && (pair || m == 1)) {
+          ++batch;
+          const Item& then = items[(i + 1) & 1];
+          if (j + kBatch < tiles) locate(it, it.c0 + j + kBatch, batch & 1);
+          else if (then.q0 >= 0) locate(then, then.c0, batch & 1);
+        }
       }
       if (!ok) break;
       n0 += tiles;
@@ -493,7 +543,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       vo[j] = rv * (uint32_t)a.rb[2] + blk32 * 16;
       vso[j] = rv * (uint32_t)a.rb[3];
     }
-    uint32_t n = 0;
+    uint32_t n = 0, batch = 0;                   // tiles and batches of places so far
     for (uint32_t i = 0;; ++i) {
       if (!__all_sync(0xffffffffu, block_wait(&bar->item_full[i & 1], (i >> 1) & 1, abort_flag))) break;
       const Item& it = items[i & 1];
@@ -502,60 +552,26 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       const uint8_t* const bks = a.base[1] + it.head * (D / 32);
       const uint8_t* const bv = a.base[2] + it.head * (D / 2);
       const uint8_t* const bvs = a.base[3] + it.head * (D / 32);
-      // pages of the two steps of a tile, looked up a tile ahead (they cost a
-      // trip to memory before the rows can be asked for)
-      Walk scout(it, a), walk(it, a);
-      int32_t page[2][4];
       // where the head's codes and scales of each step's first row are
       const uint8_t *k0, *k1, *v0, *v1, *ks0, *ks1, *vs0, *vs1;
-      bool there[2];                             // the step has rows to see, and they are in the planes
-      int32_t bad = 0;                           // bit s: step s of the tile is not there
+      int32_t flags = 0;
       Seen seen{-1, 0, 0};
-      auto wanted = [&](const Seen& w, int s) {  // a step without a row to see may have no page
-        return s * kPageStep <= w.hi && ((s + 1) * kPageStep > w.lo || s * kPageStep < w.sk);
-      };
-      auto look_up = [&](int32_t x) {
-        const int32_t p0 = scout.row(x);
-        const Seen w = Seen{scout.hi, scout.lo, a.n_sink}.from(p0);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (!wanted(w, s)) continue;
-          page[s][0] = load_page(a.map[0], a.page_shift[0], scout.seq, p0 + s * kPageStep);
-          if (!a.one_map)
-#pragma unroll
-            for (int y = 1; y < 4; ++y) page[s][y] = load_page(a.map[y], a.page_shift[y], scout.seq, p0 + s * kPageStep);
-        }
-      };
+      bool ok = true;
       auto rows_of = [&](int32_t x) {            // moves to tile x
-        const int32_t p0 = walk.row(x);
-        seen = Seen{walk.hi, walk.lo, a.n_sink}.from(p0);
-        bad = 0;
-        auto place = [&](int s, const uint8_t*& k, const uint8_t*& ks, const uint8_t*& v, const uint8_t*& vs) {
-          there[s] = false;
-          if (!wanted(seen, s)) return;
-          uint32_t r[4];                         // rows of a plane fit 31 bits
-          bool ok = true;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            if (y == 0 || !a.one_map) {
-              const int64_t b = step_base(a.map[y], a.page_shift[y], walk.seq, p0 + s * kPageStep, page[s][y], walk.hi);
-              ok = ok && b >= 0;
-              r[y] = (uint32_t)b;
-            } else {
-              r[y] = r[0];
-            }
-          }
-          there[s] = ok;
-          if (!ok) bad |= 1 << s;
-          k = bk + (uint64_t)r[0] * (uint32_t)a.rb[0];
-          ks = bks + (uint64_t)r[1] * (uint32_t)a.rb[1];
-          v = bv + (uint64_t)r[2] * (uint32_t)a.rb[2];
-          vs = bvs + (uint64_t)r[3] * (uint32_t)a.rb[3];
-        };
-        place(0, k0, ks0, v0, vs0);
-        place(1, k1, ks1, v1, vs1);
-        if (bad && fw == 0 && lane == 0) record_error(a.status, CSA2_ERR_INDEX_RANGE);
-        if (x + 1 < it.c1) look_up(x + 1);
+        const int32_t j = x - it.c0;
+        if (j % kBatch == 0) {
+          ok = __all_sync(0xffffffffu, block_wait(&bar->place_full[batch & 1], (batch >> 1) & 1, abort_flag));
+          ++batch;
+        }
+        const Place& pl = places[((batch - 1) & 1) * kBatch + j % kBatch];
+        const int4 w = *reinterpret_cast<const int4*>(&pl.seen);
+        seen = Seen{w.x, w.y, w.z};
+        flags = w.w;
+        const uint4 r0 = *reinterpret_cast<const uint4*>(pl.r[0]), r1 = *reinterpret_cast<const uint4*>(pl.r[1]);
+        k0 = bk + (uint64_t)r0.x * (uint32_t)a.rb[0], k1 = bk + (uint64_t)r1.x * (uint32_t)a.rb[0];
+        ks0 = bks + (uint64_t)r0.y * (uint32_t)a.rb[1], ks1 = bks + (uint64_t)r1.y * (uint32_t)a.rb[1];
+        v0 = bv + (uint64_t)r0.z * (uint32_t)a.rb[2], v1 = bv + (uint64_t)r1.z * (uint32_t)a.rb[2];
+        vs0 = bvs + (uint64_t)r0.w * (uint32_t)a.rb[3], vs1 = bvs + (uint64_t)r1.w * (uint32_t)a.rb[3];
       };
       uint4 kc[PER], vc[PER];
       uint32_t ks[PER], kn[PER], vs[PER];        // scales of the K rows, of their V rows, of the V rows
@@ -563,7 +579,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         return D == 128 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p));
       };
       auto mine = [&](int g) {                   // whether this lane's row of group g is to be read
-        return g < NG && (g >= NG / 2 ? there[1] : there[0]) && seen.row(g * GR + in_g);
+        return g < NG && ((flags & 16) || ((flags >> (g >= NG / 2)) & 1 && seen.row(g * GR + in_g)));
       };
       auto load_k = [&]() {
 #pragma unroll
@@ -606,17 +622,15 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
               make_uint4(mul_f16x2(o[0], s2), mul_f16x2(o[1], s2), mul_f16x2(o[2], s2), mul_f16x2(o[3], s2));
         }
       };
-      look_up(it.c0);
       rows_of(it.c0);
+      if (!ok) break;
       load_k();
       load_v();
-      bool ok = true;
       for (int32_t x = it.c0; x < it.c1; ++x, ++n) {
         const int st = n & 1;
         const uint32_t par = ((n >> 1) & 1) ^ 1;
         ok = __all_sync(0xffffffffu, block_wait(&bar->k_empty[st], par, abort_flag));
         if (!ok) break;
-        if (fw == 0 && lane == 0) bad_s[(n % kBadRing) * 2] = bad & 1, bad_s[(n % kBadRing) * 2 + 1] = bad >> 1;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
           const int g = fw + j * kFillWarps;
@@ -634,6 +648,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         if (lane == 0) mbar_arrive(&bar->k_full[st]);
         if (x + 1 < it.c1) {
           rows_of(x + 1);
+          if (!ok) break;
           load_k();
         }
         ok = __all_sync(0xffffffffu, block_wait(&bar->v_empty[st], par, abort_flag));
@@ -660,7 +675,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
     const int m = warp >> 2, r = tid & 127;      // height, row of it
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t s_t = tmem + m * kT + lanes, o_t = tmem + 256 + m * D + lanes;
-    uint32_t n_all = 0, n_s = 0, n_o = 0, n_pair = 0;   // tiles so far, of all and of this height; outputs; shared items
+    uint32_t n_batch = 0, n_s = 0, n_o = 0, n_pair = 0;   // batches of places so far; this height's tiles, outputs, shared items
     for (uint32_t i = 0;; ++i) {
       if (!__all_sync(0xffffffffu, block_wait(&bar->item_full[i & 1], (i >> 1) & 1, abort_flag))) break;
       const Item& it = items[i & 1];
@@ -709,17 +724,17 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       const Seen mine = seen_rows(pos, a.window, a.n_sink);
       float mo = -INFINITY;
       float2 l = make_float2(0.f, 0.f);
-      Walk walk(it, a);
       for (int32_t x = x0; x < c1; x += step, ++n_s) {
-        const int32_t p0 = walk.row(x);
-        // what this row sees of the tile: everything, or by a mask
-        const bool in_run = pos >= 0 && qr >= walk.qa && qr < walk.qb;
-        const Seen w = mine.from(p0);
-        const uint32_t t = n_all + (uint32_t)(x - it.c0);
         ok = __all_sync(0xffffffffu, ok && block_wait(&bar->s_full[m], n_s & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
-        const int32_t bad0 = bad_s[(t % kBadRing) * 2], bad1 = bad_s[(t % kBadRing) * 2 + 1];
+        // what this row sees of the tile: everything, or by a mask
+        const int32_t j = x - it.c0;
+        const Place& pl = places[((n_batch + j / kBatch) & 1) * kBatch + j % kBatch];
+        const int4 rq = *reinterpret_cast<const int4*>(&pl.row);
+        const bool in_run = pos >= 0 && qr >= rq.y && qr < rq.z;
+        const Seen w = mine.from(rq.x);
+        const int32_t bad0 = pl.flags & 4, bad1 = pl.flags & 8;
         const bool full = __all_sync(0xffffffffu, in_run && w.all(kT) && !(bad0 | bad1));
         // bits of columns [32 y, 32 y + 32) seen: c <= hi && (c >= lo || c < sk)
         auto below = [](int32_t k) { return k <= 0 ? 0u : (k >= 32 ? ~0u : (1u << k) - 1u); };
@@ -809,7 +824,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         if (!ok) break;
         tc_fence_after();
       }
-      n_all += (uint32_t)(c1 - it.c0);
+      n_batch += (uint32_t)(c1 - it.c0 + kBatch - 1) / kBatch;
       float sum = l.x + l.y, scale = 1.f;
       if (pair) {
         // the second height's maximum, sum and O join the first's, in the space of Q
