@@ -357,7 +357,7 @@ int32_t csa2_kv_append_fp4_bf16(const uint16_t* q, const uint16_t* k, const uint
 
 size_t csa2_gqa_attn_workspace(int32_t nq, int32_t Hq, int32_t Hkv, int32_t D) {
   if (nq < 1 || nq > 16384 || !kv_shape_ok(Hq, Hkv, D) || Hq < 1 || Hq % Hkv) return 0;
-  return gqa_scratch_bytes(nq, Hq, Hkv, D);
+  return gqa_scratch_bytes(Hq, Hkv, D);
 }
 
 static int32_t run_gqa_attn(const uint16_t* q, const csa2_kv_cache* cache, const int32_t* seq_of_query,

@@ -381,10 +381,9 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
     all = total * a.groups;
     run = div_run(all + a.n_cta - 1, a.n_cta);
     const int64_t u = (int64_t)blockIdx.x * run;
-    if (blockIdx.x == 0 || (start * a.groups <= u && u < (start + n) * a.groups)) {
+    if (start * a.groups <= u && u < (start + n) * a.groups) {
       for (int i = i0; i < i1; ++i) {
         const int64_t c = tile_range<kRows>(__ldg(a.query_pos + i), a.window, a.n_sink).count;
-        if (blockIdx.x == 0) a.starts[i] = start;
         if (start * a.groups <= u && u < (start + c) * a.groups) {
           item_s = i;
           item_start_s = start;
@@ -392,7 +391,8 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
         start += c;
       }
     }
-    if (blockIdx.x == 0 && tid == 0) a.starts[a.nq] = total, a.starts[a.nq + 1] = run;
+    write_empties<kGqaThreads>(a, D);
+    if (tid == 0) a.joints[blockIdx.x].i0 = -1;
     __syncthreads();
     if (u >= all) return;
   }
@@ -413,6 +413,8 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
     const int64_t i_start = q_start + (int64_t)grp * ur.count, i_end = i_start + ur.count;
     const int32_t c0 = (int32_t)(u - i_start), c1 = (int32_t)(min(u_end, i_end) - i_start);
     const int32_t seq = a.seq_of_query ? __ldg(a.seq_of_query + qi) : qi;
+    if (tid == 0 && i_start < u_begin && i_start >= u_begin - run)
+      a.joints[blockIdx.x] = GqaJoint{i_start, i_end, run, qi, 1, grp};
 
     // ---- this warp's head and tiles
     const int vh0 = grp * a.per_cta, n_vh = min(a.per_cta, a.vh - vh0);
@@ -562,12 +564,13 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
   }
 }
 
-// Joins the parts of every item that several CTAs share, and writes the
-// outputs of queries that see no row.  W warps work on one query head of one
-// query: the parts' weights first, then their rows, eight of a warp's in
-// flight.  Latency is all there is to it (a serial walk over 128 parts took
-// 24 us): eight warps per row where there are few rows, one where there are
-// many, whose parts are few.
+// Joins the parts of every item that several CTAs share: block (x, y) some
+// rows of the y-th of them, found by the CTA that starts in its middle first.
+// W warps work on one row: the parts' weights first, then their rows, eight
+// of a warp's in flight.  Latency is all there is to it (a serial walk over
+// 128 parts took 24 us, and a block per output row of a long chunk 105 us):
+// eight warps per row where there are few rows, one where there are many,
+// whose parts are few.
 constexpr int kCombWarps = 8;
 template <int D, int W>
 __global__ void __launch_bounds__(kCombWarps * 32) gqa_combine_kernel(const __grid_constant__ GqaArgs a,
@@ -577,32 +580,55 @@ __global__ void __launch_bounds__(kCombWarps * 32) gqa_combine_kernel(const __gr
   __shared__ float acc_s[W > 1 ? W : 1][D];
   __shared__ float w_s[R][kMaxCtas];
   __shared__ float m_s[kCombWarps], l_s[kCombWarps];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wr = warp % W, rr = warp / W;
-  const int Hq = a.Hkv * a.G;
-  const int64_t at = (int64_t)blockIdx.x * R + rr;     // row of the output
-  const bool live = at < (int64_t)a.nq * Hq;
-  const int qi = live ? (int)(at / Hq) : 0, r = live ? (int)(at % Hq) : 0;
-  const int vh = (r / a.G) * a.subs + (r % a.G) / run_heads, grp = vh / a.per_cta;
-  const int block = a.q_tile > 0 ? qi / a.q_tile : qi, n_block = a.q_tile > 0 ? (a.nq + a.q_tile - 1) / a.q_tile : a.nq;
+  __shared__ int32_t joint_s, count_s[2 * kCombWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wr = warp % W, rr = warp / W;
   pdl_wait();
-  if (!live) return;
-  const int64_t before = __ldcg(a.starts + block), run = __ldcg(a.starts + n_block + 1);
-  const int64_t count = __ldcg(a.starts + block + 1) - before;
-  if (count == 0) {
-    for (int i = wr * 32 + lane; i < D / 2; i += W * 32) reinterpret_cast<uint32_t*>(a.out + at * D)[i] = 0u;
-    if (wr == 0 && lane == 0 && a.lse) a.lse[at] = -INFINITY;
-    return;
+  int joint = 1;                                       // one item: the second CTA starts in it, or it is whole
+  if (gridDim.y == 1) {
+    if (__ldcg(&a.joints[1].i0) < 0) return;
+  } else {
+    // the y-th CTA whose first item began in the CTA before it
+    static_assert(kMaxCtas <= 2 * kCombWarps * 32, "two CTAs per thread");
+    if (tid == 0) joint_s = -1;
+    uint32_t own[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = i * kCombWarps * 32 + tid;
+      own[i] = __ballot_sync(0xffffffffu, c > 0 && c < a.n_cta && __ldcg(&a.joints[c].i0) >= 0);
+      if (lane == 0) count_s[i * kCombWarps + warp] = __popc(own[i]);
+    }
+    __syncthreads();
+    int before = 0;
+#pragma unroll
+    for (int i = 0; i < 2 * kCombWarps; ++i) {
+      const int k = i / kCombWarps;
+      if (i % kCombWarps == warp && ((own[k] >> lane) & 1u) &&
+          before + __popc(own[k] & ((1u << lane) - 1u)) == (int)blockIdx.y)
+        joint_s = k * kCombWarps * 32 + tid;
+      before += count_s[i];
+    }
+    __syncthreads();
+    joint = joint_s;
+    if (joint < 0) return;
   }
-  const int64_t i0 = before * a.groups + grp * count;
-  const int first = (int)div_run(i0, run), parts = (int)div_run(i0 + count - 1, run) - first + 1;
-  if (parts == 1) return;                              // one CTA had the whole item
-  const int rows = a.q_tile > 0 ? kBlockRows : a.per_cta * run_heads;
-  const int row = a.q_tile > 0 ? (qi % a.q_tile) * min(run_heads, a.G - (vh % a.subs) * run_heads) + (r % a.G) % run_heads
-                               : (vh - grp * a.per_cta) * run_heads + (r % a.G) % run_heads;
+  const GqaJoint jt = a.joints[joint];
+  const int first = joint - 1, parts = (int)div_run(jt.i1 - 1, jt.run) - first + 1;
+  const int rows = a.q_tile > 0 ? kBlockRows : a.per_cta * run_heads, row = blockIdx.x * R + rr;
+  // where the row goes
+  int64_t at = -1;
+  if (a.q_tile > 0) {
+    const int r0 = jt.grp % a.subs * run_heads, gs = min(run_heads, a.G - r0), q = row / gs;
+    if (q < jt.n_q)
+      at = (int64_t)(jt.q0 + q) * (a.Hkv * a.G) + jt.grp / a.subs * a.G + r0 + row % gs;
+  } else {
+    const int vh = jt.grp * a.per_cta + row / run_heads, h = vh % a.subs * run_heads + row % run_heads;
+    if (row < rows && vh < a.vh && h < a.G) at = (int64_t)jt.q0 * (a.Hkv * a.G) + vh / a.subs * a.G + h;
+  }
+  if (at < 0) return;                                  // W == kCombWarps: the block is one row
   // part p: the first CTA's last part, then each CTA's first
   auto part = [&](int p) { return (int64_t)(2 * (first + p) + (p == 0 ? 1 : 0)) * rows + row; };
   auto block_sync = [&]() {
-    if (W > 1) __syncthreads();                        // W == kCombWarps: the block is one row
+    if (W > 1) __syncthreads();
     else __syncwarp();
   };
   float M = -INFINITY;
@@ -693,7 +719,7 @@ cudaError_t launch_gqa_t(GqaArgs& a, cudaStream_t st) {
   gqa_split_kernel<D, NT><<<a.n_cta, kGqaThreads, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_gqa_combine(a, D, 8 * NT, st);
+  return launch_gqa_combine(a, D, 8 * NT, (int64_t)a.nq * a.groups, st);
 }
 
 // How query heads map to warps: runs of 8 NT heads of a KV head, up to 8 runs per CTA.
@@ -707,27 +733,29 @@ void gqa_heads(GqaArgs& a, int32_t Hkv, int32_t G, int* nt) {
   a.per_cta = (a.vh + a.groups - 1) / a.groups;
 }
 
-void carve_gqa(GqaArgs& a, Carver& c, int32_t nq, int32_t D, int nt) {
+void carve_gqa(GqaArgs& a, Carver& c, int32_t D, int nt) {
   const size_t parts = 2 * (size_t)kMaxCtas * a.per_cta * 8 * nt;
-  a.starts = c.take<int64_t>((size_t)nq + 2);
+  a.joints = c.take<GqaJoint>(kMaxCtas);
   a.part_o = c.take<float>(parts * D);
   a.part_ml = c.take<float2>(parts);
 }
 
 // The block kernel's parts: one CTA per SM, kBlockRows rows each.
-void carve_block(GqaArgs& a, Carver& c, int32_t nq, int32_t D) {
+void carve_block(GqaArgs& a, Carver& c, int32_t D) {
   const size_t parts = (size_t)kMaxCtas * kBlockRows;
-  a.starts = c.take<int64_t>((size_t)nq + 2);
+  a.joints = c.take<GqaJoint>(kMaxCtas);
   a.part_o = c.take<float>(parts * D);
   a.part_ml = c.take<float2>(parts);
 }
 
 }  // namespace
 
-cudaError_t launch_gqa_combine(const GqaArgs& a, int32_t D, int32_t run_heads, cudaStream_t st) {
-  const int64_t rows = (int64_t)a.nq * a.Hkv * a.G;
-  const bool few = rows <= 4 * sm_count();
-  const dim3 grid((unsigned)(few ? rows : (rows + kCombWarps - 1) / kCombWarps)), block(kCombWarps * 32);
+cudaError_t launch_gqa_combine(const GqaArgs& a, int32_t D, int32_t run_heads, int64_t items, cudaStream_t st) {
+  if (a.n_cta < 2) return cudaSuccess;
+  const int64_t shared = items < a.n_cta - 1 ? items : a.n_cta - 1;    // items that two CTAs can share
+  const int64_t rows = a.q_tile > 0 ? kBlockRows : a.per_cta * run_heads;
+  const bool few = shared * rows <= 4 * sm_count();
+  const dim3 grid((unsigned)(few ? rows : (rows + kCombWarps - 1) / kCombWarps), (unsigned)shared), block(kCombWarps * 32);
   if (D == 128)
     return few ? launch_k(gqa_combine_kernel<128, kCombWarps>, grid, block, 0, st, false, true, a, run_heads)
                : launch_k(gqa_combine_kernel<128, 1>, grid, block, 0, st, false, true, a, run_heads);
@@ -735,13 +763,13 @@ cudaError_t launch_gqa_combine(const GqaArgs& a, int32_t D, int32_t run_heads, c
              : launch_k(gqa_combine_kernel<64, 1>, grid, block, 0, st, false, true, a, run_heads);
 }
 
-size_t gqa_scratch_bytes(int32_t nq, int32_t Hq, int32_t Hkv, int32_t D) {
+size_t gqa_scratch_bytes(int32_t Hq, int32_t Hkv, int32_t D) {
   GqaArgs a{};
   int nt;
   gqa_heads(a, Hkv, Hq / Hkv, &nt);
   Carver c(nullptr), b(nullptr);
-  carve_gqa(a, c, nq, D, nt);
-  carve_block(a, b, nq, D);
+  carve_gqa(a, c, D, nt);
+  carve_block(a, b, D);
   return (c.used > b.used ? c.used : b.used) + 256;
 }
 
@@ -754,8 +782,8 @@ cudaError_t launch_gqa_attn(const uint16_t* q, const csa2_kv_cache& kv, const in
   const bool blocks = group_queries && nq > 1;
   gqa_heads(a, kv.Hkv, Hq / kv.Hkv, &nt);
   Carver c(ws);
-  if (blocks) carve_block(a, c, nq, kv.D);
-  else carve_gqa(a, c, nq, kv.D, nt);
+  if (blocks) carve_block(a, c, kv.D);
+  else carve_gqa(a, c, kv.D, nt);
   a.q = q, a.out = out, a.lse = lse;
   const csa2_rows* views[4] = {&kv.k_codes, &kv.k_scales, &kv.v_codes, &kv.v_scales};
   a.one_map = 1;

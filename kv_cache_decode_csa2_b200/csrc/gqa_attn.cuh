@@ -20,6 +20,13 @@ namespace csa2 {
 
 constexpr int kPageStep = 64;      // pages are multiples of this many rows
 
+// The item that a CTA's run starts in the middle of.
+struct GqaJoint {
+  int64_t i0, i1;                  // the item's tiles (i0 < 0: it did not begin in the CTA before, or there is none)
+  int64_t run;                     // tiles per CTA
+  int32_t q0, n_q, grp;            // its queries and which of their items it is
+};
+
 struct GqaArgs {
   const uint16_t* q;               // bf16 [nq][Hq][D]
   uint16_t* out;                   // bf16 [nq][Hq][D]
@@ -39,7 +46,7 @@ struct GqaArgs {
   int32_t subs;                    // runs per KV head
   int32_t per_cta;                 // virtual heads per CTA
   int32_t groups;                  // items per query or block: ceil(vh / per_cta)
-  int64_t* starts;                 // tiles of one group before each query or block, their number, tiles per CTA
+  GqaJoint* joints;                // [n_cta] what each CTA shares with the one before it
   float* part_o;                   // [2 n_cta][rows][D] unnormalised O of a part
   float2* part_ml;                 // [2 n_cta][rows] (offset max in log2 units, sum)
   int32_t* status;
@@ -131,8 +138,26 @@ __device__ __forceinline__ int64_t div_run(int64_t a, int64_t b) {
   return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
 }
 
-// Joins the parts that CTAs left (gqa_attn.cu); launched behind either kernel.
-cudaError_t launch_gqa_combine(const GqaArgs& a, int32_t D, int32_t run_heads, cudaStream_t st);
+// Joins the parts that CTAs left (gqa_attn.cu), of at most `items` items;
+// launched behind either kernel.
+cudaError_t launch_gqa_combine(const GqaArgs& a, int32_t D, int32_t run_heads, int64_t items, cudaStream_t st);
+// Outputs of this CTA's share of the queries that see no row, by all of its
+// N threads.
+template <int N>
+__device__ __forceinline__ void write_empties(const GqaArgs& a, int32_t D) {
+  const int64_t Hq = (int64_t)a.Hkv * a.G;
+  for (int64_t base = blockIdx.x; base < a.nq; base += (int64_t)a.n_cta * N) {
+    const int64_t mine = base + (int64_t)a.n_cta * threadIdx.x;
+    if (!__syncthreads_or(mine < a.nq && __ldg(a.query_pos + mine) < 0)) continue;
+    for (int64_t q = base; q < a.nq && q < base + (int64_t)a.n_cta * N; q += a.n_cta) {
+      if (__ldg(a.query_pos + q) >= 0) continue;
+      for (int64_t i = threadIdx.x; i < Hq * D / 8; i += N)
+        reinterpret_cast<uint4*>(a.out + q * Hq * D)[i] = make_uint4(0, 0, 0, 0);
+      if (a.lse)
+        for (int64_t i = threadIdx.x; i < Hq; i += N) a.lse[q * Hq + i] = -INFINITY;
+    }
+  }
+}
 // Blocks of queries on the tensor cores (gqa_block.cu): the fields of a that
 // describe the work, the CTAs at most and the rows of a part; the launch.
 constexpr int kBlockRows = 256;    // query rows of an item: two MMA heights

@@ -2,8 +2,9 @@
 // the rows they read (a prefill chunk, a speculative block), on the
 // 5th-generation tensor cores.
 //
-// An item is a block of consecutive queries with one KV head: up to 256 rows
-// (query, head of the group), two MMA heights.  It walks 128-row cache tiles:
+// An item is a run of consecutive queries of one sequence with one KV head: up
+// to 256 rows (query, head of the group), two MMA heights.  It walks 128-row
+// cache tiles:
 //   S_m [128 rows][128 positions] = Q_m K^T      (tcgen05, f16 -> fp32 in TMEM)
 //   P_m = exp2(S_m scale - max + offset)          (f16, over S_m's columns)
 //   O_m [128 rows][D] += P_m V                   (A operand from TMEM)
@@ -19,8 +20,8 @@
 // issued by the softmax warps themselves the heights fell into step, and an
 // issuing warp was late for its own tile.  An item of at most 128 rows has its
 // tiles dealt out to the two heights in turn, whose results join at the end.
-// The queries of a block may belong to several sequences: each run of queries
-// of one sequence walks its own tiles, and the others' rows are masked there.
+// Queries are taken in blocks of as many as fit 256 rows, and a block falls
+// into the runs of its queries' sequences, one item each per KV head.
 //
 // Rows a query does not see are masked in S; a value row must also not reach
 // it through 0 x NaN, so a NaN scale in V is taken as 0 there and its row's
@@ -47,7 +48,7 @@ struct alignas(16) Place {
   Seen seen;                                     // its rows that any query of the run sees
   int32_t flags;                                 // bit s: step s is there; bit 2 + s: it should be and is not; bit 4: all rows
   uint32_t r[2][4];                              // first physical row of each step in each plane
-  int32_t row, qa, qb, pad;                      // its first row; the run's queries [qa, qb) of the block
+  int32_t row, pad[3];                           // its first row
 };
 
 // The runs of a block: consecutive queries of one sequence.
@@ -57,10 +58,8 @@ struct Runs {
   int32_t q[kMaxRuns + 1];                       // its first query, relative to the block
 };
 struct Item {
-  Runs runs;
-  int32_t cum[kMaxRuns + 1];                     // tiles before each run
-  int32_t n_runs;
-  int32_t q0, n_q;                               // queries (q0 < 0: no more items)
+  int32_t q0, n_q;                               // its queries (q0 < 0: no more items)
+  int32_t seq, hi, lo;                           // their sequence and rows
   int32_t head, r0, gs;                          // KV head, first query head of the run of heads, their number
   int32_t c0, c1;                                // tiles of the item that are this CTA's
   int32_t slot;                                  // where its part goes (-1: the whole item)
@@ -70,7 +69,8 @@ template <int D>
 struct BlockSmem {
   static constexpr int kPlane = kT * D * 2;      // an f16 tile: [D / 64][128 rows][128 bytes], 128B swizzle
   static constexpr int q = 0, k = 2 * kPlane, v = k + 2 * kPlane, items = v + 2 * kPlane;
-  static constexpr int places = (items + 2 * (int)sizeof(Item) + 15) / 16 * 16;
+  static constexpr int runs = items + 2 * (int)sizeof(Item), cum = runs + (int)sizeof(Runs);
+  static constexpr int places = (cum + (kMaxRuns + 1) * 4 + 15) / 16 * 16;
   static constexpr int bars = places + 2 * kBatch * (int)sizeof(Place);
   static constexpr int total = bars + 32 * 8 + 64;
 };
@@ -321,17 +321,14 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
     run = div_run(all + a.n_cta - 1, a.n_cta);
     const int64_t u = (int64_t)blockIdx.x * run;
     for (int b = b0; b < b1; ++b) {
-      if (blockIdx.x == 0) a.starts[b] = start;
       if (start * a.groups <= u && u < (start + counts[b]) * a.groups) {
         first_s = b;
         first_start_s = start;
       }
       start += counts[b];
     }
-    if (blockIdx.x == 0 && tid == 0) {
-      a.starts[n_blocks] = total;
-      a.starts[n_blocks + 1] = run;
-    }
+    write_empties<kBlockThreads>(a, D);
+    if (tid == 0) a.joints[blockIdx.x].i0 = -1;
     __syncthreads();
   }
   const int64_t u_begin = min((int64_t)blockIdx.x * run, all), u_end = min(u_begin + run, all);
@@ -339,9 +336,13 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
 
   if (warp == kIssueWarp) {
     // ================================================== MMA issue, item lists
-    int blk = u_begin < u_end ? first_s : 0;
+    int blk = u_begin < u_end ? first_s : 0, listed = -1, n_runs = 0;
+    int32_t count = 0;                           // tiles of the block listed, for one head
     int64_t blk_start = u_begin < u_end ? first_start_s * a.groups : 0, u = u_begin;
+    Runs& runs = *reinterpret_cast<Runs*>(sm + L::runs);
+    int32_t* cum = reinterpret_cast<int32_t*>(sm + L::cum);        // tiles before each run
     // Writes the item at u into slot s (by the whole warp) and moves u past it.
+    // A block's items go run by run, head by head.
     auto build = [&](int s) {
       Item& it = items[s];
       if (u >= u_end) {
@@ -349,27 +350,40 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         __syncwarp();
         return;
       }
-      int32_t n_q, count, n_runs;
       while (true) {
-        n_q = min(a.q_tile, a.nq - blk * a.q_tile);
-        count = list_runs(a, blk * a.q_tile, n_q, it.runs, it.cum, &n_runs);
+        if (listed != blk) {
+          count = list_runs(a, blk * a.q_tile, min(a.q_tile, a.nq - blk * a.q_tile), runs, cum, &n_runs);
+          listed = blk;
+        }
         if (u < blk_start + (int64_t)count * a.groups) break;
         blk_start += (int64_t)count * a.groups;
         ++blk;
       }
-      const int grp = (int)div_run(u - blk_start, count);
-      const int64_t i_start = blk_start + (int64_t)grp * count, i_end = i_start + count;
+      int k = 0, last = n_runs - 1;              // the run: cum <= tile < cum of the next
+      const int64_t in_block = u - blk_start;
+      while (k < last) {
+        const int mid = (k + last + 1) >> 1;
+        if ((int64_t)cum[mid] * a.groups <= in_block) k = mid;
+        else last = mid - 1;
+      }
+      const int32_t n = cum[k + 1] - cum[k];
+      const int grp = (int)div_run(in_block - (int64_t)cum[k] * a.groups, n);
+      const int64_t i_start = blk_start + (int64_t)cum[k] * a.groups + (int64_t)grp * n, i_end = i_start + n;
       if (lane == 0) {
         const int sub = grp % a.subs;
-        it.n_runs = n_runs;
-        it.q0 = blk * a.q_tile;
-        it.n_q = n_q;
+        it.q0 = blk * a.q_tile + runs.q[k];
+        it.n_q = runs.q[k + 1] - runs.q[k];
+        it.seq = runs.seq[k];
+        it.hi = runs.hi[k];
+        it.lo = runs.lo[k];
         it.head = grp / a.subs;
         it.r0 = sub * kBlockRows;
         it.gs = min(kBlockRows, a.G - sub * kBlockRows);
         it.c0 = (int32_t)(u - i_start);
         it.c1 = (int32_t)(min(u_end, i_end) - i_start);
         it.slot = i_start >= u_begin && i_end <= u_end ? -1 : 2 * (int)blockIdx.x + (i_start < u_begin ? 0 : 1);
+        if (i_start < u_begin && i_start >= u_begin - run)
+          a.joints[blockIdx.x] = GqaJoint{i_start, i_end, run, it.q0, it.n_q, grp};
       }
       u = min(u_end, i_end);
       __syncwarp();
@@ -404,19 +418,12 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       const bool in = t < it.c1;
       Place* pl = places + h * kBatch + (lane >> 1);
       bool ok = false, bad = false;
-      int k = 0;
       int32_t p0 = 0;
       Seen w{-1, 0, 0};
       if (in) {
-        int hi = it.n_runs - 1;                  // the run with cum <= t < cum of the next
-        while (k < hi) {
-          const int mid = (k + hi + 1) >> 1;
-          if (it.cum[mid] <= t) k = mid;
-          else hi = mid - 1;
-        }
-        const int32_t last = it.runs.hi[k], seq = it.runs.seq[k];
-        p0 = run_tiles(last, it.runs.lo[k], a.n_sink).row(t - it.cum[k], kT);
-        w = Seen{last, it.runs.lo[k], a.n_sink}.from(p0);
+        const int32_t last = it.hi, seq = it.seq;
+        p0 = run_tiles(last, it.lo, a.n_sink).row(t, kT);
+        w = Seen{last, it.lo, a.n_sink}.from(p0);
         // a step without a row to see may have no page
         if (s * kPageStep <= w.hi && ((s + 1) * kPageStep > w.lo || s * kPageStep < w.sk)) {
           const int32_t at = p0 + s * kPageStep;
@@ -441,8 +448,6 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         pl->seen = w;
         pl->flags = flags | ((flags & 3) == 3 && w.all(kT) ? 16 : 0);
         pl->row = p0;
-        pl->qa = it.runs.q[k];
-        pl->qb = it.runs.q[k + 1];
       }
       if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(a.status, CSA2_ERR_INDEX_RANGE);
       __syncwarp();
@@ -608,6 +613,11 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
           }
         }
       };
+      // Nothing of these loads is to be used before this point: scales taken
+      // apart where they are loaded make the warp wait there.
+      auto arrived = [&](uint4& c, uint32_t& x, uint32_t& y) {
+        asm volatile("" : "+r"(c.x), "+r"(c.y), "+r"(c.z), "+r"(c.w), "+r"(x), "+r"(y));
+      };
       // 32 codes of a row of group g times their scale to the f16 tile
       auto expand = [&](uint8_t* plane, int g, const uint4& c, uint32_t scale) {
         const uint32_t s2 = e4m3x2_to_f16x2(scale * 0x101u);
@@ -632,6 +642,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         ok = __all_sync(0xffffffffu, block_wait(&bar->k_empty[st], par, abort_flag));
         if (!ok) break;
 #pragma unroll
+        for (int j = 0; j < PER; ++j) arrived(kc[j], ks[j], kn[j]);
+#pragma unroll
         for (int j = 0; j < PER; ++j) {
           const int g = fw + j * kFillWarps;
           if (g >= NG) break;
@@ -653,6 +665,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         }
         ok = __all_sync(0xffffffffu, block_wait(&bar->v_empty[st], par, abort_flag));
         if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) arrived(vc[j], vs[j], vs[j]);
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
           const int g = vw + j * kFillWarps;
@@ -684,7 +698,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       const bool pair = rows <= 128;             // both heights hold the same rows and take every other tile
       const int at = (pair ? 0 : m * 128) + r, step = pair ? 2 : 1;
       const bool live = at < rows;
-      const int qr = live ? at / it.gs : 0;      // query of the block
+      const int qr = live ? at / it.gs : 0;      // query of the run
       const int64_t out_row = (int64_t)(it.q0 + qr) * Hq + it.head * a.G + it.r0 + (at - qr * it.gs);
       const int32_t x0 = it.c0 + (pair ? m : 0), c1 = it.c1;
       // ---- this row of Q, scaled by a power of two into f16
@@ -724,6 +738,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       const Seen mine = seen_rows(pos, a.window, a.n_sink);
       float mo = -INFINITY;
       float2 l = make_float2(0.f, 0.f);
+      const bool idle = !__any_sync(0xffffffffu, live);      // no row of this warp is anyone's
       for (int32_t x = x0; x < c1; x += step, ++n_s) {
         ok = __all_sync(0xffffffffu, ok && block_wait(&bar->s_full[m], n_s & 1, abort_flag));
         if (!ok) break;
@@ -731,15 +746,13 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         // what this row sees of the tile: everything, or by a mask
         const int32_t j = x - it.c0;
         const Place& pl = places[((n_batch + j / kBatch) & 1) * kBatch + j % kBatch];
-        const int4 rq = *reinterpret_cast<const int4*>(&pl.row);
-        const bool in_run = pos >= 0 && qr >= rq.y && qr < rq.z;
-        const Seen w = mine.from(rq.x);
+        const Seen w = live ? mine.from(pl.row) : Seen{kT, 0, 0};   // a row behind the last counts as seeing all
         const int32_t bad0 = pl.flags & 4, bad1 = pl.flags & 8;
-        const bool full = __all_sync(0xffffffffu, in_run && w.all(kT) && !(bad0 | bad1));
+        const bool full = __all_sync(0xffffffffu, w.all(kT) && !(bad0 | bad1));
         // bits of columns [32 y, 32 y + 32) seen: c <= hi && (c >= lo || c < sk)
         auto below = [](int32_t k) { return k <= 0 ? 0u : (k >= 32 ? ~0u : (1u << k) - 1u); };
         auto see = [&](int y) {
-          if (!in_run || (y < 2 ? bad0 : bad1)) return 0u;
+          if (y < 2 ? bad0 : bad1) return 0u;
           return below(w.hi + 1 - 32 * y) & (~below(w.lo - 32 * y) | below(w.sk - 32 * y));
         };
         // The weights, 32 columns at a time, over the logits' columns.  The
@@ -748,7 +761,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         // columns, taken on trust, are taken again.  (One rolled loop: the
         // code of the roles has to stay in the instruction caches together.)
 #pragma unroll 1
-        for (int y = 0; y < 4;) {
+        for (int y = idle ? 4 : 0; y < 4;) {
           uint32_t s[32];
           tmem_ld32(s_t + 32 * y, s);
           tmem_wait_ld32(s);
@@ -935,7 +948,7 @@ cudaError_t launch_block_t(GqaArgs& a, cudaStream_t st) {
   gqa_block_kernel<D><<<a.n_cta, kBlockThreads, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_gqa_combine(a, D, kBlockRows, st);
+  return launch_gqa_combine(a, D, kBlockRows, (int64_t)a.nq * a.groups, st);   // a run per query at most
 }
 
 }  // namespace

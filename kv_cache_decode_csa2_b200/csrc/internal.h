@@ -255,7 +255,7 @@ cudaError_t launch_kv_append(const void* q, const void* k, const void* v, bool f
                              uint16_t* v_out, int32_t* status, cudaStream_t st);
 
 // Grouped-query attention over the FP4 cache (gqa_attn.cu).
-size_t gqa_scratch_bytes(int32_t nq, int32_t Hq, int32_t Hkv, int32_t D);
+size_t gqa_scratch_bytes(int32_t Hq, int32_t Hkv, int32_t D);
 cudaError_t launch_gqa_attn(const uint16_t* q, const csa2_kv_cache& cache, const int32_t* seq_of_query,
                             const int32_t* query_pos, int32_t nq, int32_t Hq, int32_t window, int32_t n_sink,
                             float scale, bool group_queries, uint16_t* out, float* lse, void* ws, int32_t* status,
