@@ -528,39 +528,49 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
     // ================================================== fill: codes to f16 tiles
     // A group is 8 (D = 64: 16) rows of a tile, a lane a block of 32 codes of one of
     // them; lanes are laid out so that a quarter of a warp stores to all 32
-    // banks.  Warp f expands groups f, f + 7, ... of K and 6 - f, 13 - f, ... of V.
+    // banks.  Warp f expands groups f, f + 7, ... of K and of V; of the groups
+    // left over, the first warps take K's and the last ones V's.
     const int fw = warp - kSoftWarps;
-    constexpr int NG = D == 128 ? 16 : 8, PER = (NG + kFillWarps - 1) / kFillWarps, GR = kT / NG;
+    constexpr int NG = D == 128 ? 16 : 8, EACH = NG / kFillWarps, PER = EACH + 1, LEFT = NG - EACH * kFillWarps, GR = kT / NG;
     const int in_g = D == 128 ? ((lane >> 1) & 3) + (lane >> 4) * 4 : lane >> 1;
     const int blk32 = D == 128 ? (lane & 1) + ((lane >> 3) & 1) * 2 : lane & 1;
-    const int vw = kFillWarps - 1 - fw;
-    // Offsets of this lane's rows within a step of each plane.  Everything that
-    // does not change from tile to tile is here: with the addresses worked out
-    // per tile, the fill was longer than the softmax.
-    uint32_t ko[PER], kso[PER], kno[PER], vo[PER], vso[PER];
+    const int left = kFillWarps - 1 - fw;        // of V's left over, this one's (K's: fw)
+    auto k_group = [&](int j) { return fw + j * kFillWarps; };
+    auto v_group = [&](int j) { return j < EACH ? fw + j * kFillWarps : EACH * kFillWarps + left; };
+    static_assert(LEFT > 0 && 2 * LEFT <= kFillWarps && PER * GR <= 32 && EACH >= 1, "one warp has at most one group left over");
+    // The scales of all its rows are loaded at once, a row per lane, and handed
+    // round (loaded with each block of codes they kept the load pipe waiting).
+    const int s_group = lane / GR < EACH ? k_group(lane / GR)
+                        : lane / GR == EACH && fw < LEFT ? k_group(EACH)
+                        : lane / GR == EACH && left < LEFT ? v_group(EACH) : NG;
+    const int s_row = s_group * GR + lane % GR;
+    const uint32_t s_in = s_row & (kPageStep - 1);
+    // Everything that does not change from tile to tile is worked out here: a
+    // filling warp gets an instruction in every eight clocks or so, and with
+    // the addresses made for each load the fill took longer than the softmax.
+    uint32_t in_k[PER], in_v[PER];               // this lane's row of each group, within its step
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-      const uint32_t rk = ((fw + j * kFillWarps) * GR + in_g) & (kPageStep - 1);
-      const uint32_t rv = ((vw + j * kFillWarps) * GR + in_g) & (kPageStep - 1);
-      ko[j] = rk * (uint32_t)a.rb[0] + blk32 * 16;
-      kso[j] = rk * (uint32_t)a.rb[1];
-      kno[j] = rk * (uint32_t)a.rb[3];
-      vo[j] = rv * (uint32_t)a.rb[2] + blk32 * 16;
-      vso[j] = rv * (uint32_t)a.rb[3];
+      in_k[j] = (k_group(j) * GR + in_g) & (kPageStep - 1);
+      in_v[j] = (v_group(j) * GR + in_g) & (kPageStep - 1);
     }
+    constexpr int kNext = kFillWarps * GR * 128; // bytes from one of its groups to the next in a tile
+    uint8_t* to[4];                              // where the four chunks of its block go in K's first group
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      to[y] = sm + L::k + (blk32 >> 1) * (kT * 128) + (fw * GR + in_g) * 128 + ((((blk32 & 1) * 4 + y) ^ (in_g & 7)) << 4);
+    const int to_v_left = (v_group(EACH) - fw) * GR * 128;         // of V's group left over, from the first
+    const uint32_t my_scale = blk32 * 0x11;      // byte_perm selector: this block's scale, twice
     uint32_t n = 0, batch = 0;                   // tiles and batches of places so far
     for (uint32_t i = 0;; ++i) {
       if (!__all_sync(0xffffffffu, block_wait(&bar->item_full[i & 1], (i >> 1) & 1, abort_flag))) break;
       const Item& it = items[i & 1];
       if (it.q0 < 0) break;
-      const uint8_t* const bk = a.base[0] + it.head * (D / 2);
+      const uint8_t* const bk = a.base[0] + it.head * (D / 2) + blk32 * 16;
       const uint8_t* const bks = a.base[1] + it.head * (D / 32);
-      const uint8_t* const bv = a.base[2] + it.head * (D / 2);
+      const uint8_t* const bv = a.base[2] + it.head * (D / 2) + blk32 * 16;
       const uint8_t* const bvs = a.base[3] + it.head * (D / 32);
-      // where the head's codes and scales of each step's first row are
-      const uint8_t *k0, *k1, *v0, *v1, *ks0, *ks1, *vs0, *vs1;
-      int32_t flags = 0;
-      Seen seen{-1, 0, 0};
+      const Place* pl = nullptr;                 // of the tile whose loads are next
       bool ok = true;
       auto rows_of = [&](int32_t x) {            // moves to tile x
         const int32_t j = x - it.c0;
@@ -568,68 +578,69 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
           ok = __all_sync(0xffffffffu, block_wait(&bar->place_full[batch & 1], (batch >> 1) & 1, abort_flag));
           ++batch;
         }
-        const Place& pl = places[((batch - 1) & 1) * kBatch + j % kBatch];
-        const int4 w = *reinterpret_cast<const int4*>(&pl.seen);
-        seen = Seen{w.x, w.y, w.z};
-        flags = w.w;
-        const uint4 r0 = *reinterpret_cast<const uint4*>(pl.r[0]), r1 = *reinterpret_cast<const uint4*>(pl.r[1]);
-        k0 = bk + (uint64_t)r0.x * (uint32_t)a.rb[0], k1 = bk + (uint64_t)r1.x * (uint32_t)a.rb[0];
-        ks0 = bks + (uint64_t)r0.y * (uint32_t)a.rb[1], ks1 = bks + (uint64_t)r1.y * (uint32_t)a.rb[1];
-        v0 = bv + (uint64_t)r0.z * (uint32_t)a.rb[2], v1 = bv + (uint64_t)r1.z * (uint32_t)a.rb[2];
-        vs0 = bvs + (uint64_t)r0.w * (uint32_t)a.rb[3], vs1 = bvs + (uint64_t)r1.w * (uint32_t)a.rb[3];
+        pl = places + ((batch - 1) & 1) * kBatch + j % kBatch;
       };
       uint4 kc[PER], vc[PER];
-      uint32_t ks[PER], kn[PER], vs[PER];        // scales of the K rows, of their V rows, of the V rows
+      uint32_t ks = 0, vs = 0;                   // scales of row s_row in K and V
+      uint32_t vf[PER];                          // the V blocks' scales, twice
+      // (volatile: a plain load may be moved past the barriers to where it is used)
       auto load_scales = [&](const uint8_t* p) {
-        return D == 128 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p));
+        uint32_t r;
+        if (D == 128)
+          asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(r) : "l"(p));
+        else
+          asm volatile("{\n\t.reg .b16 t;\n\tld.global.nc.b16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(r) : "l"(p));
+        return r;
       };
-      auto mine = [&](int g) {                   // whether this lane's row of group g is to be read
-        return g < NG && ((flags & 16) || ((flags >> (g >= NG / 2)) & 1 && seen.row(g * GR + in_g)));
+      auto load_codes = [&](const uint8_t* base, uint32_t r, int64_t rb) {
+        uint4 u;
+        asm volatile("ld.global.nc.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "l"(base + (uint64_t)r * (uint32_t)rb));
+        return u;
+      };
+      auto has_k = [&](int j) { return j < EACH || fw < LEFT; };
+      auto has_v = [&](int j) { return j < EACH || left < LEFT; };
+      auto seen_row = [&](int rr) {              // whether row rr of the tile is to be read
+        const int32_t f = pl->flags;
+        return (f & 16) || ((f >> (rr >= kPageStep)) & 1 && pl->seen.row(rr));
       };
       auto load_k = [&]() {
+        ks = vs = 0;
+        if (s_group < NG && seen_row(s_row)) {
+          const uint32_t* r = pl->r[s_row >= kPageStep];
+          ks = load_scales(bks + (uint64_t)(r[1] + s_in) * (uint32_t)a.rb[1]);
+          vs = load_scales(bvs + (uint64_t)(r[3] + s_in) * (uint32_t)a.rb[3]);
+        }
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-          const int g = fw + j * kFillWarps;
-          const bool s = g >= NG / 2;
+          const int rr = k_group(j) * GR + in_g;
           kc[j] = make_uint4(0, 0, 0, 0);
-          ks[j] = kn[j] = 0;
-          if (mine(g)) {
-            kc[j] = __ldg(reinterpret_cast<const uint4*>((s ? k1 : k0) + ko[j]));
-            ks[j] = load_scales((s ? ks1 : ks0) + kso[j]);
-            kn[j] = load_scales((s ? vs1 : vs0) + kno[j]);
-          }
+          if (has_k(j) && seen_row(rr)) kc[j] = load_codes(bk, pl->r[rr >= kPageStep][0] + in_k[j], a.rb[0]);
         }
       };
       auto load_v = [&]() {
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-          const int g = vw + j * kFillWarps;
-          const bool s = g >= NG / 2;
+          const int rr = v_group(j) * GR + in_g;
           vc[j] = make_uint4(0, 0, 0, 0);
-          vs[j] = 0;
-          if (mine(g)) {
-            vc[j] = __ldg(reinterpret_cast<const uint4*>((s ? v1 : v0) + vo[j]));
-            vs[j] = load_scales((s ? vs1 : vs0) + vso[j]);
-          }
+          if (has_v(j) && seen_row(rr)) vc[j] = load_codes(bv, pl->r[rr >= kPageStep][2] + in_v[j], a.rb[2]);
         }
       };
       // Nothing of these loads is to be used before this point: scales taken
       // apart where they are loaded make the warp wait there.
-      auto arrived = [&](uint4& c, uint32_t& x, uint32_t& y) {
-        asm volatile("" : "+r"(c.x), "+r"(c.y), "+r"(c.z), "+r"(c.w), "+r"(x), "+r"(y));
-      };
-      // 32 codes of a row of group g times their scale to the f16 tile
-      auto expand = [&](uint8_t* plane, int g, const uint4& c, uint32_t scale) {
-        const uint32_t s2 = e4m3x2_to_f16x2(scale * 0x101u);
+      auto arrived = [&](uint4& c) { asm volatile("" : "+r"(c.x), "+r"(c.y), "+r"(c.z), "+r"(c.w)); };
+      // 32 codes times their scale (twice in s2's bytes) to the f16 tile, `off`
+      // bytes from K's first group
+      auto expand = [&](int off, const uint4& c, uint32_t s2) {
         const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-        const int rr = g * GR + in_g;
-        uint8_t* at = plane + (blk32 >> 1) * (kT * 128) + rr * 128;
+        const uint32_t f = e4m3x2_to_f16x2(s2);
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
           uint32_t o[4];
           e2m1x8_to_f16(w[y], o);
-          *reinterpret_cast<uint4*>(at + ((((blk32 & 1) * 4 + y) ^ (rr & 7)) << 4)) =
-              make_uint4(mul_f16x2(o[0], s2), mul_f16x2(o[1], s2), mul_f16x2(o[2], s2), mul_f16x2(o[3], s2));
+          *reinterpret_cast<uint4*>(to[y] + off) =
+              make_uint4(mul_f16x2(o[0], f), mul_f16x2(o[1], f), mul_f16x2(o[2], f), mul_f16x2(o[3], f));
         }
       };
       rows_of(it.c0);
@@ -642,18 +653,17 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         ok = __all_sync(0xffffffffu, block_wait(&bar->k_empty[st], par, abort_flag));
         if (!ok) break;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) arrived(kc[j], ks[j], kn[j]);
+        for (int j = 0; j < PER; ++j) arrived(kc[j]);
+        asm volatile("" : "+r"(ks), "+r"(vs));
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-          const int g = fw + j * kFillWarps;
-          if (g >= NG) break;
-          // any NaN scale among the row's values: the row's logits are NaN
-          uint32_t s = (ks[j] >> (8 * blk32)) & 0xFFu;
-          bool nan = false;
-#pragma unroll
-          for (int y = 0; y < D / 32; ++y) nan |= ((kn[j] >> (8 * y)) & 0x7Fu) == 0x7Fu;
-          if (nan) s = 0x7Fu;
-          expand(sm + L::k + st * L::kPlane, g, kc[j], s);
+          const uint32_t k4 = __shfl_sync(0xffffffffu, ks, (j * GR + in_g) & 31), v4 = __shfl_sync(0xffffffffu, vs, (j * GR + in_g) & 31);
+          const uint32_t v2 = __byte_perm(v4, 0, my_scale);
+          vf[j] = (v2 & 0x7Fu) == 0x7Fu ? 0u : v2;
+          if (!has_k(j)) break;
+          // any NaN scale (0x7F without its sign) among the row's values: its logits are NaN
+          const bool nan = ((v4 & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+          expand(st * L::kPlane + j * kNext, kc[j], nan ? 0x7F7Fu : __byte_perm(k4, 0, my_scale));
         }
         fence_async_smem();
         __syncwarp();
@@ -666,15 +676,10 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         ok = __all_sync(0xffffffffu, block_wait(&bar->v_empty[st], par, abort_flag));
         if (!ok) break;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) arrived(vc[j], vs[j], vs[j]);
+        for (int j = 0; j < PER; ++j) arrived(vc[j]);
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const int g = vw + j * kFillWarps;
-          if (g >= NG) break;
-          uint32_t s = (vs[j] >> (8 * blk32)) & 0xFFu;
-          if ((s & 0x7Fu) == 0x7Fu) s = 0;
-          expand(sm + L::v + st * L::kPlane, g, vc[j], s);
-        }
+        for (int j = 0; j < PER; ++j)
+          if (has_v(j)) expand(L::v - L::k + st * L::kPlane + (j < EACH ? j * kNext : to_v_left), vc[j], vf[j]);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->v_full[st]);
