@@ -171,6 +171,11 @@ __device__ __forceinline__ float2 fma2(uint32_t x0, uint32_t x1, float m, float 
       : "r"(x0), "r"(x1), "f"(m), "f"(c));
   return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void add2(float2& acc, float x0, float x1) {
   asm("{\n\t.reg .b64 x, y;\n\t"
       "mov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
@@ -570,7 +575,9 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       const uint8_t* const bks = a.base[1] + it.head * (D / 32);
       const uint8_t* const bv = a.base[2] + it.head * (D / 2) + blk32 * 16;
       const uint8_t* const bvs = a.base[3] + it.head * (D / 32);
-      const Place* pl = nullptr;                 // of the tile whose loads are next
+      Seen seen{-1, 0, 0};                       // the place of the tile whose loads are next
+      int32_t flags = 0;
+      uint4 pr[2] = {};
       bool ok = true;
       auto rows_of = [&](int32_t x) {            // moves to tile x
         const int32_t j = x - it.c0;
@@ -578,7 +585,12 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
           ok = __all_sync(0xffffffffu, block_wait(&bar->place_full[batch & 1], (batch >> 1) & 1, abort_flag));
           ++batch;
         }
-        pl = places + ((batch - 1) & 1) * kBatch + j % kBatch;
+        const Place& pl = places[((batch - 1) & 1) * kBatch + j % kBatch];
+        const int4 w = *reinterpret_cast<const int4*>(&pl.seen);
+        seen = Seen{w.x, w.y, w.z};
+        flags = w.w;
+        pr[0] = *reinterpret_cast<const uint4*>(pl.r[0]);
+        pr[1] = *reinterpret_cast<const uint4*>(pl.r[1]);
       };
       uint4 kc[PER], vc[PER];
       uint32_t ks = 0, vs = 0;                   // scales of row s_row in K and V
@@ -602,21 +614,20 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       auto has_k = [&](int j) { return j < EACH || fw < LEFT; };
       auto has_v = [&](int j) { return j < EACH || left < LEFT; };
       auto seen_row = [&](int rr) {              // whether row rr of the tile is to be read
-        const int32_t f = pl->flags;
-        return (f & 16) || ((f >> (rr >= kPageStep)) & 1 && pl->seen.row(rr));
+        return (flags & 16) || ((flags >> (rr >= kPageStep)) & 1 && seen.row(rr));
       };
       auto load_k = [&]() {
         ks = vs = 0;
         if (s_group < NG && seen_row(s_row)) {
-          const uint32_t* r = pl->r[s_row >= kPageStep];
-          ks = load_scales(bks + (uint64_t)(r[1] + s_in) * (uint32_t)a.rb[1]);
-          vs = load_scales(bvs + (uint64_t)(r[3] + s_in) * (uint32_t)a.rb[3]);
+          const bool hi = s_row >= kPageStep;
+          ks = load_scales(bks + (uint64_t)((hi ? pr[1].y : pr[0].y) + s_in) * (uint32_t)a.rb[1]);
+          vs = load_scales(bvs + (uint64_t)((hi ? pr[1].w : pr[0].w) + s_in) * (uint32_t)a.rb[3]);
         }
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
           const int rr = k_group(j) * GR + in_g;
           kc[j] = make_uint4(0, 0, 0, 0);
-          if (has_k(j) && seen_row(rr)) kc[j] = load_codes(bk, pl->r[rr >= kPageStep][0] + in_k[j], a.rb[0]);
+          if (has_k(j) && seen_row(rr)) kc[j] = load_codes(bk, (rr >= kPageStep ? pr[1].x : pr[0].x) + in_k[j], a.rb[0]);
         }
       };
       auto load_v = [&]() {
@@ -624,7 +635,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         for (int j = 0; j < PER; ++j) {
           const int rr = v_group(j) * GR + in_g;
           vc[j] = make_uint4(0, 0, 0, 0);
-          if (has_v(j) && seen_row(rr)) vc[j] = load_codes(bv, pl->r[rr >= kPageStep][2] + in_v[j], a.rb[2]);
+          if (has_v(j) && seen_row(rr)) vc[j] = load_codes(bv, (rr >= kPageStep ? pr[1].z : pr[0].z) + in_v[j], a.rb[2]);
         }
       };
       // Nothing of these loads is to be used before this point: scales taken
@@ -650,7 +661,9 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       for (int32_t x = it.c0; x < it.c1; ++x, ++n) {
         const int st = n & 1;
         const uint32_t par = ((n >> 1) & 1) ^ 1;
-        ok = __all_sync(0xffffffffu, block_wait(&bar->k_empty[st], par, abort_flag));
+        // (read now: while products read shared memory, a trip there is long)
+        if (x + 1 < it.c1) rows_of(x + 1);
+        ok = ok && __all_sync(0xffffffffu, block_wait(&bar->k_empty[st], par, abort_flag));
         if (!ok) break;
 #pragma unroll
         for (int j = 0; j < PER; ++j) arrived(kc[j]);
@@ -668,11 +681,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->k_full[st]);
-        if (x + 1 < it.c1) {
-          rows_of(x + 1);
-          if (!ok) break;
-          load_k();
-        }
+        if (x + 1 < it.c1) load_k();
         ok = __all_sync(0xffffffffu, block_wait(&bar->v_empty[st], par, abort_flag));
         if (!ok) break;
 #pragma unroll
@@ -782,7 +791,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
           for (int c = 0; c < 16; ++c) {
             const float2 v = fma2(s[2 * c], s[2 * c + 1], qs, -sub);
             s[2 * c] = __float_as_uint(v.x), s[2 * c + 1] = __float_as_uint(v.y);
-            top[c & 1] = fmaxf(top[c & 1], fmaxf(v.x, v.y));
+            top[c & 1] = max3(top[c & 1], v.x, v.y);
           }
           float2 add = make_float2(0.f, 0.f);
           uint32_t p[16];
