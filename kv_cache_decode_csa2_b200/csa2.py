@@ -448,10 +448,13 @@ class _Call:
         if torch.cuda.current_device() != self.device.index:
             raise ValueError(f"{self.name}: the cache is on {self.device}, the current device is "
                              f"cuda:{torch.cuda.current_device()}")
-        if stream is not None:
+        if stream is None:      # (current_stream() makes a Stream object: 3.4 us of a 9 us call)
+            raw = torch._C._cuda_getCurrentRawStream(self.device.index)
+        else:
+            raw = stream.cuda_stream
             for t in self.scratch:
                 t.record_stream(stream)
-        _check(self.fn(*self.args, _stream(stream)), self.name)
+        _check(self.fn(*self.args, raw), self.name)
 
 
 def _heads(t, n_heads, D, dtype, n, name) -> int:

@@ -13,11 +13,12 @@
 // row shows it; infinities saturate to the largest stored value.
 //
 // Bound by HBM: every value is read once and written once, and the table row
-// of a position is read once per slot.  A slot of D / 8 lanes owns one head
-// at a time, eight values (16 bytes of bf16) per lane: loads and stores are
-// coalesced, a block's maximum is two shuffles, and the rotation partner of
-// the half-split layout is one shuffle away.  A slot walks up to `per` heads
-// of its token with the angles in registers, kBatch heads' loads in flight.
+// of a position is read once per slot.  A slot of lanes owns one head at a
+// time.  For keys and values a lane has eight values (16 bytes of bf16): loads
+// and stores are coalesced, a block's maximum is two shuffles, and the rotation
+// partner of the half-split layout is one shuffle away; for queries, which are
+// most of the work, it has both sides of eight pairs.  A slot walks `per` heads of
+// its token with the angles in registers, kBatch heads' loads in flight.
 #include "csa2_device.cuh"
 #include "fp4_device.cuh"
 #include "internal.h"
@@ -34,7 +35,7 @@ struct AppendArgs {
   int64_t ld[3];              // row strides in values
   int32_t heads[3];           // Hq (0: no queries), Hkv, Hkv
   int32_t first[3];           // first chunk of each kind within a token
-  int32_t chunks;             // chunks of one token
+  int32_t chunks;             // chunks of a token
   int32_t per;                // heads per chunk
   int64_t n;
   const int32_t* seq_of_row;
@@ -46,6 +47,7 @@ struct AppendArgs {
   uint8_t* scales[2];
   int64_t codes_rb[2], scales_rb[2];
   RowMap cmap[2], smap[2];
+  int32_t cshift[2], sshift[2];   // log2 of the rows per page (-1: not a power of two)
   int32_t one_map;            // all four planes place rows alike
   uint16_t* q_out;            // [n][Hq][D]
   uint16_t* kv_out[2];        // [n][Hkv][D] or nullptr
@@ -54,9 +56,17 @@ struct AppendArgs {
 
 // The row of (seq, pos), refusing a position outside the sequence's own
 // share of a contiguous plane.
-__device__ __forceinline__ int64_t write_row(const RowMap& m, int32_t seq, int32_t pos) {
-  if (seq < 0 || (!m.page_table && m.seq_rows > 0 && pos >= m.seq_rows)) return -1;
-  return map_row(m, seq, pos);
+__device__ __forceinline__ int64_t write_row(const RowMap& m, int32_t shift, int32_t seq, int32_t pos) {
+  if (seq < 0) return -1;
+  int64_t r;
+  if (m.page_table) {
+    const int32_t pg = shift >= 0 ? pos >> shift : pos / m.page_rows;
+    const int32_t phys = pg < m.max_pages ? __ldg(m.page_table + (int64_t)seq * m.max_pages + pg) : -1;
+    r = phys < 0 ? -1 : (int64_t)phys * m.page_rows + (pos - pg * m.page_rows);
+  } else {
+    r = m.seq_rows > 0 && pos >= m.seq_rows ? -1 : (int64_t)seq * m.seq_rows + pos;
+  }
+  return r < m.n_rows ? r : -1;
 }
 
 template <bool F32>
@@ -107,39 +117,106 @@ __device__ __forceinline__ float turn_b(float a, float b, float c, float s) {
   return __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
 }
 
-template <int D, bool F32, bool PAIRS>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int LPH = D / 8;                      // lanes per head
-  const int64_t slot = ((int64_t)blockIdx.x * kAppendThreads + threadIdx.x) / LPH;
-  const int l = threadIdx.x % LPH, lane = threadIdx.x & 31;
-  const uint32_t mask = (LPH == 32 ? 0xffffffffu : ((1u << LPH) - 1u)) << (lane / LPH * LPH);
-  const int64_t row = slot / a.chunks;
-  if (row >= a.n) return;
-  const int ch = (int)(slot % a.chunks);
-  const int kind = ch >= a.first[2] ? 2 : (ch >= a.first[1] ? 1 : 0);   // query, key, value
-  const int h0 = (ch - a.first[kind]) * a.per;
-  const int h1 = min(h0 + a.per, a.heads[kind]);
-
-  const int32_t pos = __ldg(a.row_pos + row);
-  if (pos < 0) return;                            // a padding row
+// Where a token goes: its rows in [K, V][codes, scales].  False for a padding
+// row, and, with the error recorded, for a token out of range: a token is
+// stored whole or not at all.
+__device__ __forceinline__ bool place_token(const AppendArgs& a, int64_t row, bool report, int32_t& pos,
+                                            int64_t (&rows)[2][2]) {
+  pos = __ldg(a.row_pos + row);
+  if (pos < 0) return false;
   const int32_t seq = a.seq_of_row ? __ldg(a.seq_of_row + row) : (int32_t)row;
-  // a token is stored whole or not at all
-  int64_t rows[2][2];                             // [K, V][codes, scales]
-  bool ok = !(a.rot > 0 && pos >= a.n_pos);
-  rows[0][0] = write_row(a.cmap[0], seq, pos);
-  rows[0][1] = a.one_map ? rows[0][0] : write_row(a.smap[0], seq, pos);
-  rows[1][0] = a.one_map ? rows[0][0] : write_row(a.cmap[1], seq, pos);
-  rows[1][1] = a.one_map ? rows[0][0] : write_row(a.smap[1], seq, pos);
-  ok = ok && rows[0][0] >= 0 && rows[0][1] >= 0 && rows[1][0] >= 0 && rows[1][1] >= 0;
-  if (!ok) {
-    if (l == 0) record_error(a.status, CSA2_ERR_INDEX_RANGE);
-    return;
-  }
+  rows[0][0] = write_row(a.cmap[0], a.cshift[0], seq, pos);
+  rows[0][1] = a.one_map ? rows[0][0] : write_row(a.smap[0], a.sshift[0], seq, pos);
+  rows[1][0] = a.one_map ? rows[0][0] : write_row(a.cmap[1], a.cshift[1], seq, pos);
+  rows[1][1] = a.one_map ? rows[0][0] : write_row(a.smap[1], a.sshift[1], seq, pos);
+  const bool ok = !(a.rot > 0 && pos >= a.n_pos) && rows[0][0] >= 0 && rows[0][1] >= 0 && rows[1][0] >= 0 &&
+                  rows[1][1] >= 0;
+  if (!ok && report) record_error(a.status, CSA2_ERR_INDEX_RANGE);
+  return ok;
+}
 
+__device__ __forceinline__ void load_angles(const float* t, int half, float (&co)[8], float (&si)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 c4 = __ldg(reinterpret_cast<const float4*>(t) + i);
+    const float4 s4 = __ldg(reinterpret_cast<const float4*>(t + half) + i);
+    co[4 * i] = c4.x, co[4 * i + 1] = c4.y, co[4 * i + 2] = c4.z, co[4 * i + 3] = c4.w;
+    si[4 * i] = s4.x, si[4 * i + 1] = s4.y, si[4 * i + 2] = s4.z, si[4 * i + 3] = s4.w;
+  }
+}
+
+// Queries: a lane has sixteen values of a head, of the half-split layout both
+// sides of eight pairs, so that the rotation asks nothing of other lanes.
+template <int D, bool F32, bool PAIRS>
+__device__ __forceinline__ void append_queries(const AppendArgs& a, uint32_t tokens, int chunk) {
+  constexpr int LPH = D / 16, QB = F32 ? 1 : 2;   // lanes per head; heads whose loads are in flight
+  const int64_t row = ((int64_t)tokens * kAppendThreads + threadIdx.x) / LPH;
+  const int l = threadIdx.x % LPH;
+  if (row >= a.n) return;
+  int32_t pos;
+  int64_t rows[2][2];
+  if (!place_token(a, row, l == 0, pos, rows)) return;
+  const int half = a.rot / 2;
+  const bool turned = l * 16 < a.rot;
+  const int first = PAIRS || !turned ? l * 16 : l * 8, second = PAIRS || !turned ? first + 8 : first + half;
+  float co[8], si[8];
+  if (turned) load_angles(a.cos_sin + (int64_t)pos * a.rot + l * 8, half, co, si);
+  const int h0 = chunk * a.per, h1 = min(h0 + a.per, a.heads[0]);
+  const int64_t in = row * a.ld[0], out = row * a.heads[0] * D;
+  for (int hb = h0; hb < h1; hb += QB) {
+    Raw<F32> raw[QB][2];
+#pragma unroll
+    for (int j = 0; j < QB; ++j)
+      if (hb + j < h1) {
+        raw[j][0] = load8<F32>(a.x[0], in + (hb + j) * D + first);
+        raw[j][1] = load8<F32>(a.x[0], in + (hb + j) * D + second);
+      }
+#pragma unroll
+    for (int j = 0; j < QB; ++j) {
+      if (hb + j >= h1) break;
+      float v[2][8];
+      widen<F32>(raw[j][0], v[0]);
+      widen<F32>(raw[j][1], v[1]);
+      if (turned) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float& x = PAIRS ? v[e / 4][2 * (e % 4)] : v[0][e];
+          float& y = PAIRS ? v[e / 4][2 * (e % 4) + 1] : v[1][e];
+          const float nx = turn_a(x, y, co[e], si[e]);
+          y = turn_b(x, y, co[e], si[e]);
+          x = nx;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const __nv_bfloat162 b = __floats2bfloat162_rn(v[i][2 * e], v[i][2 * e + 1]);
+          w[e] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(a.q_out + out + (hb + j) * D + (i ? second : first)) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+}
+
+// Keys (KV = 0) or values (KV = 1): a lane has eight values of a head.
+template <int D, bool F32, bool PAIRS, int KV>
+__device__ __forceinline__ void append_rows(const AppendArgs& a, uint32_t tokens, int chunk) {
+  constexpr int LPH = D / 8;
+  const int64_t row = ((int64_t)tokens * kAppendThreads + threadIdx.x) / LPH;
+  const int l = threadIdx.x % LPH, lane = threadIdx.x & 31;
+  const uint32_t mask = ((1u << LPH) - 1u) << (lane / LPH * LPH);
+  if (row >= a.n) return;
+  const int h0 = (chunk - a.first[1 + KV]) * a.per, h1 = min(h0 + a.per, a.heads[1 + KV]);
+  int32_t pos;
+  int64_t rows[2][2];
+  if (!place_token(a, row, l == 0, pos, rows)) return;
   // this lane's angles: eight of the half-split layout (values l*8..l*8+7 are
   // one side of eight pairs), four of the interleaved one
   const int half = a.rot / 2;
-  const bool turned = kind < 2 && l * 8 < a.rot;
+  const bool turned = KV == 0 && l * 8 < a.rot;
   const bool low = l * 8 < half;
   const int partner = !turned || PAIRS ? l : (low ? l + half / 8 : l - half / 8);
   constexpr int NA = PAIRS ? 4 : 8;
@@ -159,14 +236,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
     Raw<F32> raw[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j)
-      if (hb + j < h1) raw[j] = load8<F32>(a.x[kind], row * a.ld[kind] + (int64_t)(hb + j) * D + l * 8);
+      if (hb + j < h1) raw[j] = load8<F32>(a.x[1 + KV], row * a.ld[1 + KV] + (hb + j) * D + l * 8);
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int h = hb + j;
       if (h >= h1) break;                         // uniform in the slot
       float v[8];
       widen<F32>(raw[j], v);
-      if (!PAIRS && kind < 2 && a.rot > 0) {
+      if (!PAIRS && KV == 0 && a.rot > 0) {
         float o[8];
         widen<F32>(from_lane<F32>(mask, raw[j], partner, LPH), o);
         if (turned) {
@@ -183,16 +260,6 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
           v[2 * e + 1] = turn_b(x, y, co[e], si[e]);
         }
       }
-      if (kind == 0) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * e], v[2 * e + 1]);
-          w[e] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        *reinterpret_cast<uint4*>(a.q_out + (row * a.heads[0] + h) * D + l * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-        continue;
-      }
       // magnitudes compare as their bits, with a NaN above everything
       uint32_t top = 0;
 #pragma unroll
@@ -205,7 +272,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
         const float s = e4m3_pos(sb);
         if (s > 0.f) {
           const float r = 1.0f / s;
-          const bool wide = F32 || (kind == 1 && a.rot > 0);   // more than bf16's 8 significant bits
+          const bool wide = F32 || (KV == 0 && a.rot > 0);   // more than bf16's 8 significant bits
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             if (top == 0x7F800000u) v[e] = fminf(fmaxf(v[e], -2688.f), 2688.f);
@@ -215,23 +282,39 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const __grid_
           w = e2m1x8(v);
         }
       }
-      const int kv = kind - 1;
-      *reinterpret_cast<uint32_t*>(a.codes[kv] + rows[kv][0] * a.codes_rb[kv] + h * (D / 2) + l * 4) = w;
-      if ((l & 3) == 0) a.scales[kv][rows[kv][1] * a.scales_rb[kv] + h * (D / 32) + l / 4] = (uint8_t)sb;
-      if (a.kv_out[kv]) {
+      *reinterpret_cast<uint32_t*>(a.codes[KV] + rows[KV][0] * a.codes_rb[KV] + h * (D / 2) + l * 4) = w;
+      if ((l & 3) == 0) a.scales[KV][rows[KV][1] * a.scales_rb[KV] + h * (D / 32) + l / 4] = (uint8_t)sb;
+      if (a.kv_out[KV]) {
         uint32_t o[4];
         dequant8(w, sb, o);
-        *reinterpret_cast<uint4*>(a.kv_out[kv] + (row * a.heads[kind] + h) * D + l * 8) =
+        *reinterpret_cast<uint4*>(a.kv_out[KV] + (row * a.heads[1 + KV] + h) * D + l * 8) =
             make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
 }
 
+template <int D, bool F32, bool PAIRS>
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+  // chunks of the same tokens are neighbours: their rows lie together, and the
+  // arithmetic of keys and values runs beside the queries' traffic
+  const uint32_t tokens = blockIdx.x / (uint32_t)a.chunks;
+  const int chunk = (int)(blockIdx.x - tokens * (uint32_t)a.chunks);
+  if (chunk < a.first[1]) append_queries<D, F32, PAIRS>(a, tokens, chunk);
+  else if (chunk < a.first[2]) append_rows<D, F32, PAIRS, 0>(a, tokens, chunk);
+  else append_rows<D, F32, PAIRS, 1>(a, tokens, chunk);
+}
+
 template <int D, bool F32>
 void launch_append_t(const AppendArgs& a, bool pairs, unsigned grid, cudaStream_t st) {
   if (pairs) kv_append_kernel<D, F32, true><<<grid, kAppendThreads, 0, st>>>(a);
   else kv_append_kernel<D, F32, false><<<grid, kAppendThreads, 0, st>>>(a);
+}
+
+int32_t page_shift(const csa2_rows& v) {
+  for (int b = 6; b < 31; ++b)
+    if (v.page_table && v.page_rows == 1 << b) return b;
+  return -1;
 }
 
 }  // namespace
@@ -265,28 +348,34 @@ cudaError_t launch_kv_append(const void* q, const void* k, const void* v, bool f
     a.scales_rb[i] = sc[i]->row_bytes;
     a.cmap[i] = to_rowmap(*cd[i]);
     a.smap[i] = to_rowmap(*sc[i]);
+    a.cshift[i] = page_shift(*cd[i]);
+    a.sshift[i] = page_shift(*sc[i]);
   }
   a.one_map = same_rows(c.k_codes, c.k_scales) && same_rows(c.k_codes, c.v_codes) && same_rows(c.k_codes, c.v_scales);
   a.q_out = q_out;
   a.kv_out[0] = k_out;
   a.kv_out[1] = v_out;
   a.status = status;
-  // One head per slot while the launch cannot fill the device, four when it can.
+  // One head per slot while the launch cannot fill the device; when it can,
+  // enough heads that a slot's own reading (row, page, angles) is the smaller
+  // part of what it reads (2,048 tokens of 64 + 2 x 8 heads: 27.4 us with four
+  // heads per slot, 26.0 us with sixteen).
   const int lph = c.D / 8;
-  const int64_t heads = (int64_t)n * (Hq + 2 * c.Hkv);
-  a.per = heads * lph <= (int64_t)sm_count() * 2048 ? 1 : kBatch;
+  const int64_t lanes = (int64_t)n * (Hq + 2 * c.Hkv) * lph, full = (int64_t)sm_count() * 2048;
+  a.per = lanes <= full ? 1 : lanes <= 8 * full ? kBatch : 4 * kBatch;
   a.first[0] = 0;
   a.first[1] = (Hq + a.per - 1) / a.per;
   a.first[2] = a.first[1] + (c.Hkv + a.per - 1) / a.per;
   a.chunks = a.first[2] + (c.Hkv + a.per - 1) / a.per;
-  const int64_t grid = ((int64_t)n * a.chunks * lph + kAppendThreads - 1) / kAppendThreads;
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const int64_t blocks = ((int64_t)n * lph + kAppendThreads - 1) / kAppendThreads * a.chunks;
+  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  const unsigned grid = (unsigned)blocks;
   if (c.D == 128) {
-    if (f32) launch_append_t<128, true>(a, interleaved, (unsigned)grid, st);
-    else launch_append_t<128, false>(a, interleaved, (unsigned)grid, st);
+    if (f32) launch_append_t<128, true>(a, interleaved, grid, st);
+    else launch_append_t<128, false>(a, interleaved, grid, st);
   } else {
-    if (f32) launch_append_t<64, true>(a, interleaved, (unsigned)grid, st);
-    else launch_append_t<64, false>(a, interleaved, (unsigned)grid, st);
+    if (f32) launch_append_t<64, true>(a, interleaved, grid, st);
+    else launch_append_t<64, false>(a, interleaved, grid, st);
   }
   return cudaGetLastError();
 }
