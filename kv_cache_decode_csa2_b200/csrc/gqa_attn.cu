@@ -54,6 +54,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // has its halves swapped for the same end), and four bytes of scales per row.
 constexpr int kRows = 32;
 constexpr int kStages = 3;
+// Tiles a CTA takes at least: one each makes as many parts as there are tiles
+// to join.  A query over 4,096 rows takes 19.1, 16.8, 17.3, 18.8, 21.2 us with
+// 1, 2, 3, 4, 6.
+constexpr int kMinRun = 2;
 template <int D>
 struct GqaRing {
   static constexpr int kRow = D / 2;
@@ -368,6 +372,7 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
   __shared__ int32_t item_s;
   __shared__ int64_t item_start_s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  pdl_wait();      // launched while the grid before it drains: 2.4 us less per call
   pdl_trigger();
 
   // ---- where this CTA's run of tiles starts
@@ -379,7 +384,7 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
     for (int i = i0; i < i1; ++i) n += tile_range<kRows>(__ldg(a.query_pos + i), a.window, a.n_sink).count;
     int64_t start = block_scan(n, scan_s, &total);
     all = total * a.groups;
-    run = div_run(all + a.n_cta - 1, a.n_cta);
+    run = max(div_run(all + a.n_cta - 1, a.n_cta), (int64_t)kMinRun);
     const int64_t u = (int64_t)blockIdx.x * run;
     if (start * a.groups <= u && u < (start + n) * a.groups) {
       for (int i = i0; i < i1; ++i) {
@@ -716,8 +721,7 @@ cudaError_t launch_gqa_t(GqaArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   a.n_cta = sm_count() * (NT == 1 ? 2 : 1);
   if (a.n_cta > kMaxCtas) a.n_cta = kMaxCtas;
-  gqa_split_kernel<D, NT><<<a.n_cta, kGqaThreads, smem, st>>>(a);
-  e = cudaGetLastError();
+  e = launch_k(gqa_split_kernel<D, NT>, dim3(a.n_cta), dim3(kGqaThreads), smem, st, false, true, a);
   if (e != cudaSuccess) return e;
   return launch_gqa_combine(a, D, 8 * NT, (int64_t)a.nq * a.groups, st);
 }

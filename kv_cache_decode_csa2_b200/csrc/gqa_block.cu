@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
   static_assert(sizeof(Bars) <= 32 * 8, "barriers");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_blocks = (a.nq + a.q_tile - 1) / a.q_tile;
+  pdl_wait();      // launched while the grid before it drains
   pdl_trigger();
 
   // ---- prologue: barriers, TMEM, and where this CTA's run of tiles starts
@@ -959,8 +960,7 @@ cudaError_t launch_block_t(GqaArgs& a, cudaStream_t st) {
   static_assert(kCountWarps * (int)sizeof(Runs) + 16384 * 4 <= BlockSmem<D>::items, "the prologue's counts fit the tiles");
   cudaError_t e = ensure_smem(gqa_block_kernel<D>, smem, done);
   if (e != cudaSuccess) return e;
-  gqa_block_kernel<D><<<a.n_cta, kBlockThreads, smem, st>>>(a);
-  e = cudaGetLastError();
+  e = launch_k(gqa_block_kernel<D>, dim3(a.n_cta), dim3(kBlockThreads), smem, st, false, true, a);
   if (e != cudaSuccess) return e;
   return launch_gqa_combine(a, D, kBlockRows, (int64_t)a.nq * a.groups, st);   // a run per query at most
 }

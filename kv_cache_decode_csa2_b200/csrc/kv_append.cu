@@ -296,6 +296,7 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, uint32_t tokens
 
 template <int D, bool F32, bool PAIRS>
 __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+  pdl_wait();      // launched while the grid before it drains
   // chunks of the same tokens are neighbours: their rows lie together, and the
   // arithmetic of keys and values runs beside the queries' traffic
   const uint32_t tokens = blockIdx.x / (uint32_t)a.chunks;
@@ -306,9 +307,9 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const __gr
 }
 
 template <int D, bool F32>
-void launch_append_t(const AppendArgs& a, bool pairs, unsigned grid, cudaStream_t st) {
-  if (pairs) kv_append_kernel<D, F32, true><<<grid, kAppendThreads, 0, st>>>(a);
-  else kv_append_kernel<D, F32, false><<<grid, kAppendThreads, 0, st>>>(a);
+cudaError_t launch_append_t(const AppendArgs& a, bool pairs, unsigned grid, cudaStream_t st) {
+  if (pairs) return launch_k(kv_append_kernel<D, F32, true>, dim3(grid), dim3(kAppendThreads), 0, st, false, true, a);
+  return launch_k(kv_append_kernel<D, F32, false>, dim3(grid), dim3(kAppendThreads), 0, st, false, true, a);
 }
 
 int32_t page_shift(const csa2_rows& v) {
@@ -370,14 +371,9 @@ cudaError_t launch_kv_append(const void* q, const void* k, const void* v, bool f
   const int64_t blocks = ((int64_t)n * lph + kAppendThreads - 1) / kAppendThreads * a.chunks;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   const unsigned grid = (unsigned)blocks;
-  if (c.D == 128) {
-    if (f32) launch_append_t<128, true>(a, interleaved, grid, st);
-    else launch_append_t<128, false>(a, interleaved, grid, st);
-  } else {
-    if (f32) launch_append_t<64, true>(a, interleaved, grid, st);
-    else launch_append_t<64, false>(a, interleaved, grid, st);
-  }
-  return cudaGetLastError();
+  if (c.D == 128)
+    return f32 ? launch_append_t<128, true>(a, interleaved, grid, st) : launch_append_t<128, false>(a, interleaved, grid, st);
+  return f32 ? launch_append_t<64, true>(a, interleaved, grid, st) : launch_append_t<64, false>(a, interleaved, grid, st);
 }
 
 }  // namespace csa2
