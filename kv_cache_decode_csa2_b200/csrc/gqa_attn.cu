@@ -54,6 +54,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 // has its halves swapped for the same end), and four bytes of scales per row.
 constexpr int kRows = 32;
 constexpr int kStages = 3;
+static_assert(kRows == 32 && kStages == 3, "a lane per row of scales, written a turn before they are read");
 // Tiles a CTA takes at least: one each makes as many parts as there are tiles
 // to join.  A query over 4,096 rows takes 19.1, 16.8, 17.3, 18.8, 21.2 us with
 // 1, 2, 3, 4, 6.

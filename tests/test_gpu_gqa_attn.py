@@ -338,3 +338,61 @@ def test_shards_of_a_context_combine():
     spread = np.abs(cache.values("v", 0, np.arange(600))).max()
     assert (out.double() - whole.double()).abs().max().item() <= 4 * 2.0 ** -8 * spread
     assert torch.allclose(lse, whole_lse, rtol=2.0 ** -20, atol=2.0 ** -18)
+
+
+@pytest.mark.parametrize("group", [False, True])
+@pytest.mark.parametrize("Hq,Hkv", [(300, 1), (514, 2)])
+def test_groups_of_more_heads_than_a_block_holds(Hq, Hkv, group):
+    rng = np.random.default_rng(17)
+    cache = Cache(rng, 2, 150, Hkv, 64, paged=True)
+    seq, pos = [0, 0, 1, 1], [148, 149, 3, -1]
+    q, q64 = queries(rng, 4, Hq, 64)
+    for window, n_sink in ((0, 0), (30, 2)):
+        out, lse = attend(cache, q, seq, pos, window, n_sink, group_queries=group)
+        check_attention(cache, q64, seq, pos, out, lse, window, n_sink)
+
+
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (700, 5)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [3, 8])
+def test_runs_of_many_sizes_in_one_call(G, D, window, n_sink):
+    """Runs of 1 to 33 queries in one call, over few rows and over many that
+    several CTAs share: every fill of a block, from one row to all of it, next
+    to every other."""
+    rng = np.random.default_rng(G + D)
+    sizes = [1, 5, 8, 9, 16, 17, 32, 33, 2, 21, 7, 22]
+    lens = [2900, 6000, 40, 1200, 5, 17, 700, 33, 4000, 21, 7, 22]
+    rng.shuffle(lens)
+    lens = [max(n, r) for n, r in zip(lens, sizes)]
+    cache = Cache(rng, len(sizes), max(lens), 2, D, paged=True, lens=lens)
+    seq = [s for s, r in enumerate(sizes) for _ in range(r)]
+    pos = [lens[s] - r + i for s, r in enumerate(sizes) for i in range(r)]
+    q, q64 = queries(rng, len(pos), 2 * G, D)
+    out, lse = attend(cache, q, seq, pos, window, n_sink, group_queries=True)
+    check_attention(cache, q64, seq, pos, out, lse, window, n_sink, only=range(0, len(pos), 3))
+    again, lse2 = attend(cache, q, seq, pos, window, n_sink, group_queries=True)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("group", [False, True])
+def test_two_handles_on_two_streams(group):
+    """Calls in flight together, each with the workspace of its own handle."""
+    rng = np.random.default_rng(18)
+    cache = Cache(rng, 2, 2500, 2, 128, paged=True)
+    seq, pos = [0, 0, 1, 1], [2498, 2499, 1000, 1001]
+    calls = []
+    for _ in range(2):
+        q, q64 = queries(rng, 4, 16, 128)
+        out = torch.empty((4, 16, 128), dtype=torch.bfloat16, device=DEV)
+        lse = torch.empty((4, 16), device=DEV)
+        h = B.GqaAttn(cache.c, q.to(DEV), torch.tensor(pos, dtype=torch.int32, device=DEV), out, lse=lse,
+                      seq_of_query=torch.tensor(seq, dtype=torch.int32, device=DEV), group_queries=group)
+        calls.append((h, q64, out, lse, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for h, _, _, _, st in calls:
+            h.run(stream=st)
+    torch.cuda.synchronize()
+    for h, q64, out, lse, _ in calls:
+        B.check_status(h.status)
+        check_attention(cache, q64, seq, pos, out, lse)
