@@ -489,13 +489,15 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       if (lane == 0) mbar_arrive(&bar->item_full[(i + 1) & 1]);
       // batches: P V of a tile, then Q K^T of the height's next.  The operands
       // are waited for before P: while an S product reads shared memory at its
-      // full rate, a barrier there takes hundreds of clocks.
+      // full rate, a barrier there takes hundreds of clocks.  Heights that take
+      // every other tile wait for K last (201 -> 169 us for 8 blocks of 5
+      // queries: V of the tile after next was filled later for it).
       const uint32_t step = pair ? 2 : 1, batches = pair ? tiles : 2 * tiles;
       for (uint32_t b = 0; b < batches && ok; ++b) {
         const int m = b & 1;
         const uint32_t j = pair ? b : b >> 1, n = n0 + j, nn = n + step;
         const bool more = j + step < tiles, last_use = pair || m == 1;
-        ok = wait(&bar->v_full[n & 1], (n >> 1) & 1) && (!more || wait(&bar->k_full[nn & 1], (nn >> 1) & 1)) &&
+        ok = wait(&bar->v_full[n & 1], (n >> 1) & 1) && (pair || !more || wait(&bar->k_full[nn & 1], (nn >> 1) & 1)) &&
              wait(&bar->p_full[m], n_p[m] & 1);
         if (!ok) break;
         ++n_p[m];
@@ -503,14 +505,20 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         if (elect_one()) {
           values(m, n, j < step);
           if (last_use) mma_commit(&bar->v_empty[n & 1]);
-          if (more) {
-            logits(m, nn);
-            if (last_use) mma_commit(&bar->k_empty[nn & 1]);
-          } else {
+          if (!more) {
             mma_commit(&bar->o_full[m]);
+          } else {
+            if (pair) {
+              ok = block_wait(&bar->k_full[nn & 1], (nn >> 1) & 1, abort_flag);
+              tc_fence_after();
+            }
+            if (ok) {
+              logits(m, nn);
+              if (last_use) mma_commit(&bar->k_empty[nn & 1]);
+            }
           }
         }
-        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
         // The first tile of a batch is through: the batch before is done with
         // (its tiles' P have all been taken), and its half of the ring is free.
         if (j % kBatch == 0 && (pair || m == 1)) {
