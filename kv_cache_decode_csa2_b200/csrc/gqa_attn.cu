@@ -571,31 +571,33 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
 }
 
 // Joins the parts of every item that several CTAs share: block (x, y) some
-// rows of the y-th of them, found by the CTA that starts in its middle first.
-// W warps work on one row: the parts' weights first, then their rows, eight
-// of a warp's in flight.  Latency is all there is to it (a serial walk over
-// 128 parts took 24 us, and a block per output row of a long chunk 105 us):
-// eight warps per row where there are few rows, one where there are many,
-// whose parts are few.
+// rows of the y-th of them, found by the CTA that starts in its middle first,
+// and of every gridDim.y-th one on.  W warps work on one row: the parts'
+// weights first, then their rows, N of a warp's in flight.  Latency is all
+// there is to it (a serial walk over 128 parts took 24 us, and a block per
+// output row of a long chunk 105 us): eight warps per row where there are few
+// rows, one where there are many, whose parts are few.  Without a number of
+// blocks asked for, the compiler keeps to 32 registers and has the rows come
+// one by one (a query over 4,096 rows: 14.2 us, with 64 registers 13.3 us).
 constexpr int kCombWarps = 8;
-template <int D, int W>
-__global__ void __launch_bounds__(kCombWarps * 32) gqa_combine_kernel(const __grid_constant__ GqaArgs a,
-                                                                      int32_t run_heads) {
+template <int D, int W, int N>
+__global__ void __launch_bounds__(kCombWarps * 32, N == 8 ? 4 : 8) gqa_combine_kernel(const __grid_constant__ GqaArgs a,
+                                                                      int32_t run_heads, bool one) {
   constexpr int R = kCombWarps / W;                    // rows per block
   constexpr int V = D / 32;                            // values per lane
   __shared__ float acc_s[W > 1 ? W : 1][D];
   __shared__ float w_s[R][kMaxCtas];
   __shared__ float m_s[kCombWarps], l_s[kCombWarps];
-  __shared__ int32_t joint_s, count_s[2 * kCombWarps];
+  __shared__ int16_t joint_s[kMaxCtas];
+  __shared__ int32_t count_s[2 * kCombWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, wr = warp % W, rr = warp / W;
   pdl_wait();
-  int joint = 1;                                       // one item: the second CTA starts in it, or it is whole
-  if (gridDim.y == 1) {
+  int n_live = 1;                                      // one item: the second CTA starts in it, or it is whole
+  if (one) {
     if (__ldcg(&a.joints[1].i0) < 0) return;
   } else {
-    // the y-th CTA whose first item began in the CTA before it
+    // the CTAs whose first item began in the CTA before them
     static_assert(kMaxCtas <= 2 * kCombWarps * 32, "two CTAs per thread");
-    if (tid == 0) joint_s = -1;
     uint32_t own[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -604,113 +606,115 @@ __global__ void __launch_bounds__(kCombWarps * 32) gqa_combine_kernel(const __gr
       if (lane == 0) count_s[i * kCombWarps + warp] = __popc(own[i]);
     }
     __syncthreads();
-    int before = 0;
+    n_live = 0;
 #pragma unroll
     for (int i = 0; i < 2 * kCombWarps; ++i) {
       const int k = i / kCombWarps;
-      if (i % kCombWarps == warp && ((own[k] >> lane) & 1u) &&
-          before + __popc(own[k] & ((1u << lane) - 1u)) == (int)blockIdx.y)
-        joint_s = k * kCombWarps * 32 + tid;
-      before += count_s[i];
+      if (i % kCombWarps == warp && ((own[k] >> lane) & 1u))
+        joint_s[n_live + __popc(own[k] & ((1u << lane) - 1u))] = (int16_t)(k * kCombWarps * 32 + tid);
+      n_live += count_s[i];
     }
     __syncthreads();
-    joint = joint_s;
-    if (joint < 0) return;
   }
-  const GqaJoint jt = a.joints[joint];
-  const int first = joint - 1, parts = (int)div_run(jt.i1 - 1, jt.run) - first + 1;
   const int rows = a.q_tile > 0 ? kBlockRows : a.per_cta * run_heads, row = blockIdx.x * R + rr;
-  // where the row goes
-  int64_t at = -1;
-  if (a.q_tile > 0) {
-    const int r0 = jt.grp % a.subs * run_heads, gs = min(run_heads, a.G - r0), q = row / gs;
-    if (q < jt.n_q)
-      at = (int64_t)(jt.q0 + q) * (a.Hkv * a.G) + jt.grp / a.subs * a.G + r0 + row % gs;
-  } else {
-    const int vh = jt.grp * a.per_cta + row / run_heads, h = vh % a.subs * run_heads + row % run_heads;
-    if (row < rows && vh < a.vh && h < a.G) at = (int64_t)jt.q0 * (a.Hkv * a.G) + vh / a.subs * a.G + h;
-  }
-  if (at < 0) return;                                  // W == kCombWarps: the block is one row
-  // part p: the first CTA's last part, then each CTA's first
-  auto part = [&](int p) { return (int64_t)(2 * (first + p) + (p == 0 ? 1 : 0)) * rows + row; };
   auto block_sync = [&]() {
     if (W > 1) __syncthreads();
     else __syncwarp();
   };
-  float M = -INFINITY;
-  for (int p = wr * 32 + lane; p < parts; p += W * 32) M = fmaxf(M, __ldcg(&a.part_ml[part(p)]).x);
+  for (int y = blockIdx.y; y < n_live; y += gridDim.y) {
+    const int joint = one ? 1 : joint_s[y];
+    const GqaJoint jt = a.joints[joint];
+    const int first = joint - 1, parts = (int)div_run(jt.i1 - 1, jt.run) - first + 1;
+    // where the row goes
+    int64_t at = -1;
+    if (a.q_tile > 0) {
+      const int r0 = jt.grp % a.subs * run_heads, gs = min(run_heads, a.G - r0), q = row / gs;
+      if (q < jt.n_q)
+        at = (int64_t)(jt.q0 + q) * (a.Hkv * a.G) + jt.grp / a.subs * a.G + r0 + row % gs;
+    } else {
+      const int vh = jt.grp * a.per_cta + row / run_heads, h = vh % a.subs * run_heads + row % run_heads;
+      if (row < rows && vh < a.vh && h < a.G) at = (int64_t)jt.q0 * (a.Hkv * a.G) + vh / a.subs * a.G + h;
+    }
+    if (at < 0) continue;                                // W == kCombWarps: the block is one row
+    // part p: the first CTA's last part, then each CTA's first
+    auto part = [&](int p) { return (int64_t)(2 * (first + p) + (p == 0 ? 1 : 0)) * rows + row; };
+    float M = -INFINITY;
+    for (int p = wr * 32 + lane; p < parts; p += W * 32) M = fmaxf(M, __ldcg(&a.part_ml[part(p)]).x);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (W > 1) {
-    if (lane == 0) m_s[warp] = M;
-    __syncthreads();
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (W > 1) {
+      if (lane == 0) m_s[warp] = M;
+      __syncthreads();
 #pragma unroll
-    for (int w = 0; w < W; ++w) M = fmaxf(M, m_s[w]);
-  }
-  float l = 0.f;
-  for (int p = wr * 32 + lane; p < parts; p += W * 32) {
-    const float2 ml = __ldcg(&a.part_ml[part(p)]);
-    // a part without a maximum saw only NaN, and its sum says so
-    const float f = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - M);
-    w_s[rr][p] = f;
-    l += f * ml.y;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  if (W > 1 && lane == 0) l_s[warp] = l;
-  block_sync();
-  float acc[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  for (int p0 = wr; p0 < parts; p0 += 8 * W) {
-    float o[8][V];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int p = p0 + i * W;
-      const float* src = a.part_o + part(p) * D + lane * V;
-#pragma unroll
-      for (int e = 0; e < V; ++e) o[i][e] = 0.f;
-      if (p < parts) {
-        if constexpr (V == 4) {
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-          o[i][0] = v.x, o[i][1] = v.y, o[i][2] = v.z, o[i][3] = v.w;
-        } else {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-          o[i][0] = v.x, o[i][1] = v.y;
-        }
-      }
+      for (int w = 0; w < W; ++w) M = fmaxf(M, m_s[w]);
+    }
+    float l = 0.f;
+    for (int p = wr * 32 + lane; p < parts; p += W * 32) {
+      const float2 ml = __ldcg(&a.part_ml[part(p)]);
+      // a part without a maximum saw only NaN, and its sum says so
+      const float f = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - M);
+      w_s[rr][p] = f;
+      l += f * ml.y;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int p = p0 + i * W;
-      const float f = p < parts ? w_s[rr][p] : 0.f;
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] += f * o[i][e];
-    }
-  }
-  if (W > 1) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc_s[wr][lane * V + i] = acc[i];
-    __syncthreads();
-    if (wr > 0) return;
-    l = 0.f;
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (W > 1 && lane == 0) l_s[warp] = l;
+    block_sync();
+    float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int p0 = wr; p0 < parts; p0 += N * W) {
+      float o[N][V];
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      l += l_s[w];
+      for (int i = 0; i < N; ++i) {
+        const int p = p0 + i * W;
+        const float* src = a.part_o + part(p) * D + lane * V;
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += acc_s[w][lane * V + i];
+        for (int e = 0; e < V; ++e) o[i][e] = 0.f;
+        if (p < parts) {
+          if constexpr (V == 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+            o[i][0] = v.x, o[i][1] = v.y, o[i][2] = v.z, o[i][3] = v.w;
+          } else {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+            o[i][0] = v.x, o[i][1] = v.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int p = p0 + i * W;
+        const float f = p < parts ? w_s[rr][p] : 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] += f * o[i][e];
+      }
     }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * D) + lane * (V / 2);
+    if (W > 1) {
 #pragma unroll
-  for (int i = 0; i < V / 2; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    dst[i] = *reinterpret_cast<const uint32_t*>(&b);
+      for (int i = 0; i < V; ++i) acc_s[wr][lane * V + i] = acc[i];
+      __syncthreads();
+      l = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        l += l_s[w];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += acc_s[w][lane * V + i];
+      }
+    }
+    if (W == 1 || wr == 0) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + at * D) + lane * (V / 2);
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+        dst[i] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+      if (lane == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
+    }
+    block_sync();                                      // shared memory is free for the next
   }
-  if (lane == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
 }
 
 template <int D, int NT>
@@ -760,12 +764,16 @@ cudaError_t launch_gqa_combine(const GqaArgs& a, int32_t D, int32_t run_heads, i
   const int64_t shared = items < a.n_cta - 1 ? items : a.n_cta - 1;    // items that two CTAs can share
   const int64_t rows = a.q_tile > 0 ? kBlockRows : a.per_cta * run_heads;
   const bool few = shared * rows <= 4 * sm_count();
-  const dim3 grid((unsigned)(few ? rows : (rows + kCombWarps - 1) / kCombWarps), (unsigned)shared), block(kCombWarps * 32);
-  if (D == 128)
-    return few ? launch_k(gqa_combine_kernel<128, kCombWarps>, grid, block, 0, st, false, true, a, run_heads)
-               : launch_k(gqa_combine_kernel<128, 1>, grid, block, 0, st, false, true, a, run_heads);
-  return few ? launch_k(gqa_combine_kernel<64, kCombWarps>, grid, block, 0, st, false, true, a, run_heads)
-             : launch_k(gqa_combine_kernel<64, 1>, grid, block, 0, st, false, true, a, run_heads);
+  // Most of a block of queries' rows and most CTAs' joints may be nobody's: blocks for all of them take longer to come
+  // and go than the others to join, so one wave of them goes on from item to item, with two parts in flight for eight
+  // blocks per SM (five blocks of 77 queries: 25.1 us with all blocks, 23.7 us so; a chunk of 4,096 280 and 276 us).
+  const int64_t x = few ? rows : (rows + kCombWarps - 1) / kCombWarps, most = 8 * sm_count() / x;
+  const dim3 grid((unsigned)x, (unsigned)(shared < most || few ? shared : most)), block(kCombWarps * 32);
+  const bool one = items == 1;
+  auto launch = [&](auto kernel) { return launch_k(kernel, grid, block, 0, st, false, true, a, run_heads, one); };
+  if (few) return D == 128 ? launch(gqa_combine_kernel<128, kCombWarps, 8>) : launch(gqa_combine_kernel<64, kCombWarps, 8>);
+  if (a.q_tile > 0) return D == 128 ? launch(gqa_combine_kernel<128, 1, 2>) : launch(gqa_combine_kernel<64, 1, 2>);
+  return D == 128 ? launch(gqa_combine_kernel<128, 1, 8>) : launch(gqa_combine_kernel<64, 1, 8>);
 }
 
 size_t gqa_scratch_bytes(int32_t Hq, int32_t Hkv, int32_t D) {
