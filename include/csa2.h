@@ -389,10 +389,12 @@ typedef struct csa2_kv_cache {
  *               (2i, 2i+1) if `interleaved`, else (i, i + rot/2):
  *               a' = a cos - b sin, b' = b cos + a sin, in fp32
  *   q_out       bf16 [n][Hq][D]; may be q itself in the bf16 call (ld_q = Hq D)
- *   k_out, v_out  bf16 [n][Hkv][D] or NULL: the values as stored (code x scale)
+ *   k_out, v_out  bf16 [n][Hkv][D] or NULL: the values as stored (code x scale);
+ *               may be k and v themselves as q_out may be q
  * Keys and values are quantised as csa2_fp4_quantize does, from fp32; further,
  * a block that holds a NaN is stored with the NaN scale 0x7F and zero codes,
- * and infinities as +-6 x 448.  A token whose position or row is out of range
+ * and infinities as +-6 x 448.  Keys and values need planes of their own
+ * (CSA2_ERR_INVALID_ARG).  A token whose position or row is out of range
  * is not stored at all (CSA2_ERR_INDEX_RANGE).  Two tokens of one call must
  * not name the same position of a sequence: the row would hold a mix.
  * Supported: D in {64, 128}; 1 <= Hkv <= 256; 0 <= Hq <= 1024; rot a multiple
@@ -423,7 +425,9 @@ int32_t csa2_kv_append_fp4_bf16(const uint16_t* q, const uint16_t* k, const uint
  *   out          bf16 [nq][Hq][D];  lse float [nq][Hq] or NULL, as
  *                csa2_sparse_attn_fp4 (parts combine with csa2_attn_combine)
  * Accumulation is fp32.  No value of a row that a query does not see reaches
- * its output, whatever bytes the row holds.  Supported: D in {64, 128}; Hq a
+ * its output, whatever bytes the row holds; of a row that it does see, a NaN
+ * among the keys makes the head's output NaN, and one among the values at
+ * least the output's values beside it (with group_queries all D).  Supported: D in {64, 128}; Hq a
  * multiple of Hkv; 1 <= Hkv <= 256; Hq <= 1024; 1 <= nq <= 16384.
  */
 int32_t csa2_gqa_attn_fp4(const uint16_t* q, const csa2_kv_cache* cache, const int32_t* seq_of_query,

@@ -330,6 +330,14 @@ static int32_t run_kv_append(const void* q, const void* k, const void* v, bool f
     return CSA2_ERR_INVALID_ARG;
   if (rot > 0 && (!cos_sin || !aligned(cos_sin, 16) || n_pos < 1)) return CSA2_ERR_INVALID_ARG;
   if (!aligned(k_out, 16) || !aligned(v_out, 16)) return CSA2_ERR_INVALID_ARG;
+  // keys and values stored over one another; outputs over inputs of another layout, which other tokens still read
+  if (cache->k_codes.base == cache->v_codes.base || cache->k_scales.base == cache->v_scales.base)
+    return CSA2_ERR_INVALID_ARG;
+  const auto over = [&](const void* x, int64_t ld, int64_t width, const void* out) {
+    return out && out == x && (f32 || ld != width);
+  };
+  if (over(q, ld_q, (int64_t)Hq * cache->D, q_out) || over(k, ld_k, kv, k_out) || over(v, ld_v, kv, v_out))
+    return CSA2_ERR_INVALID_ARG;
   return cuda_status(launch_kv_append(q, k, v, f32, n, Hq, ld_q, ld_k, ld_v, seq_of_row, row_pos, cos_sin, n_pos,
                                       rot, interleaved != 0, *cache, q_out, k_out, v_out, status,
                                       static_cast<cudaStream_t>(stream)));

@@ -31,12 +31,12 @@ def _cache(Hkv=8, D=128, **change):
     c = B.csa2_kv_cache()
     c.Hkv, c.D = Hkv, D
     for name, w in (("k_codes", D // 2), ("k_scales", D // 32), ("v_codes", D // 2), ("v_scales", D // 32)):
-        setattr(c, name, change.get(name, _rows(Hkv * w)))
+        setattr(c, name, change.get(name, _rows(Hkv * w, base=A + (1 << 20) * (name[0] == "v"))))
     return c
 
 
 def _append(c, bf16=False, q=A, k=A, v=A, n=4, Hq=64, ld_q=8192, ld_k=1024, ld_v=1024, seq=None, pos=A, cos=A, n_pos=9,
-            rot=128, q_out=A, k_out=None, v_out=None, status=A):
+            rot=128, q_out=A + 64, k_out=None, v_out=None, status=A):
     fn = K.lib().csa2_kv_append_fp4_bf16 if bf16 else K.lib().csa2_kv_append_fp4
     return fn(q, k, v, n, Hq, ld_q, ld_k, ld_v, seq, pos, cos, n_pos, rot, 0, ctypes.byref(c) if c else None, q_out,
               k_out, v_out, status, None)
@@ -69,6 +69,11 @@ def test_append_refuses_bad_arguments():
                 _cache(k_scales=_rows(32, n_rows=0)), _cache(k_codes=_rows(512, table=A, page_rows=32, max_pages=2)),
                 _cache(v_scales=_rows(32, table=A, page_rows=64, max_pages=0)), _cache(k_codes=_rows(512, seq_rows=-1))):
         assert _append(bad) == 1
+    for name, w in (("v_codes", 512), ("v_scales", 32)):         # keys and values in one plane
+        assert _append(_cache(**{name: _rows(w)})) == 1
+    # an output over an input of another layout
+    assert _append(c, ld_q=8200, q_out=A, bf16=True) == 1 and _append(c, q_out=A) == 1
+    assert _append(c, k_out=A) == 1 and _append(c, v_out=A, ld_v=1032, bf16=True) == 1
     assert _append(c, n=0, k=None, v=None, pos=None, q=None, Hq=0, q_out=None) == 0     # nothing to do
 
 
