@@ -39,7 +39,9 @@ constexpr int kIssueWarp = kSoftWarps + kFillWarps;
 constexpr int kWarps = kIssueWarp + 1;
 constexpr int kBlockThreads = 32 * kWarps;
 constexpr int kMaxRuns = 256;                    // runs of a block, at most one per query
-constexpr int kCountWarps = 7;                   // warps that count tiles in the prologue (their scratch is shared memory)
+// Warps that count tiles in the prologue; their scratch is the tiles' space, which at D = 64 has room for seven.
+template <int D>
+constexpr int kCountWarps = D == 128 ? kWarps : 7;
 constexpr int kBatch = 16;                       // tiles whose places are worked out together
 
 // Where a tile is: worked out kBatch tiles at a time, a lane per step of 64
@@ -289,11 +291,11 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
-  int32_t* counts = reinterpret_cast<int32_t*>(sm + kCountWarps * sizeof(Runs));
-  if (warp >= kWarps - kCountWarps) {
-    const int cw = warp - (kWarps - kCountWarps);
+  int32_t* counts = reinterpret_cast<int32_t*>(sm + kCountWarps<D> * sizeof(Runs));
+  if (warp >= kWarps - kCountWarps<D>) {
+    const int cw = warp - (kWarps - kCountWarps<D>);
     Runs& scratch = reinterpret_cast<Runs*>(sm)[cw];
-    for (int b = cw; b < n_blocks; b += kCountWarps) {
+    for (int b = cw; b < n_blocks; b += kCountWarps<D>) {
       int32_t n_runs;
       const int32_t c = list_runs(a, b * a.q_tile, min(a.q_tile, a.nq - b * a.q_tile), scratch, nullptr, &n_runs);
       if (lane == 0) counts[b] = c;
@@ -965,7 +967,7 @@ cudaError_t launch_block_t(GqaArgs& a, cudaStream_t st) {
   static SetupMask done{0};
   constexpr int smem = BlockSmem<D>::total + 1024 + 64;
   static_assert(smem <= 227 * 1024, "shared memory");
-  static_assert(kCountWarps * (int)sizeof(Runs) + 16384 * 4 <= BlockSmem<D>::items, "the prologue's counts fit the tiles");
+  static_assert(kCountWarps<D> * (int)sizeof(Runs) + 16384 * 4 <= BlockSmem<D>::items, "the prologue's counts fit the tiles");
   cudaError_t e = ensure_smem(gqa_block_kernel<D>, smem, done);
   if (e != cudaSuccess) return e;
   e = launch_k(gqa_block_kernel<D>, dim3(a.n_cta), dim3(kBlockThreads), smem, st, false, true, a);
