@@ -19,6 +19,10 @@
 // partner of the half-split layout is one shuffle away; for queries, which are
 // most of the work, it has both sides of eight pairs.  A slot walks `per` heads of
 // its token with the angles in registers, kBatch heads' loads in flight.
+//
+// Measured on 64 query and 8 KV heads, D = 128, bf16: 32,768 tokens 272 us
+// (1.38 GB, 5.07 TB/s, 0.77 of the copy rate), 2,048 tokens 23.8 us (3.66
+// TB/s), 32 tokens 6.9 us, which is the launch.  What is left waits for loads.
 #include "csa2_device.cuh"
 #include "fp4_device.cuh"
 #include "internal.h"
