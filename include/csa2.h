@@ -416,7 +416,9 @@ int32_t csa2_kv_append_fp4_bf16(const uint16_t* q, const uint16_t* k, const uint
  * sees.  Query head h reads KV head h / (Hq / Hkv).
  *   q            bf16 [nq][Hq][D]
  *   query_pos    int32 [nq]; a query sees rows 0..query_pos[i]; a negative
- *                position sees none: its output is 0 and its lse -inf
+ *                position sees none: its output is 0 and its lse -inf; one
+ *                past the rows that a plane has for a sequence, or past 2^29 - 1,
+ *                is CSA2_ERR_INDEX_RANGE and sees the rows before
  *   softmax_scale  host; <= 0 means 1/sqrt(D)
  *   group_queries  nonzero: consecutive queries of one sequence share the rows
  *                they read (a prefill chunk, a speculative block); zero: every

@@ -517,7 +517,8 @@ class KVAppend(_Call):
 
 class GqaAttn(_Call):
     """A marshalled csa2_gqa_attn_fp4 (or, with ``window``,
-    csa2_gqa_window_attn_fp4) call with a workspace of its own."""
+    csa2_gqa_window_attn_fp4) call with a workspace of its own: calls that are
+    in flight together, on two streams, need a handle each."""
 
     def __init__(self, cache: KVCache, q, query_pos, out, *, seq_of_query=None, window: int = 0, n_sink: int = 0,
                  softmax_scale: float = 0.0, lse=None, group_queries: bool = False, status=None, ws=None):

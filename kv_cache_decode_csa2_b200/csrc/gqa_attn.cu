@@ -36,6 +36,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "fp4_device.cuh"
 #include "gqa_attn.cuh"
 
@@ -393,14 +395,14 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
     const int per = (a.nq + kGqaThreads - 1) / kGqaThreads;
     const int i0 = min(tid * per, a.nq), i1 = min(i0 + per, a.nq);
     int64_t n = 0;
-    for (int i = i0; i < i1; ++i) n += tile_range<kRows>(__ldg(a.query_pos + i), a.window, a.n_sink).count;
+    for (int i = i0; i < i1; ++i) n += tile_range<kRows>(position(a, i), a.window, a.n_sink).count;
     int64_t start = block_scan(n, scan_s, &total);
     all = total * a.groups;
     run = max(div_run(all + a.n_cta - 1, a.n_cta), (int64_t)kMinRun);
     const int64_t u = (int64_t)blockIdx.x * run;
     if (start * a.groups <= u && u < (start + n) * a.groups) {
       for (int i = i0; i < i1; ++i) {
-        const int64_t c = tile_range<kRows>(__ldg(a.query_pos + i), a.window, a.n_sink).count;
+        const int64_t c = tile_range<kRows>(position(a, i), a.window, a.n_sink).count;
         if (start * a.groups <= u && u < (start + c) * a.groups) {
           item_s = i;
           item_start_s = start;
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
   int qi = item_s;
   int64_t q_start = item_start_s * a.groups;       // first tile of the query, over its groups
   for (int64_t u = u_begin; u < u_end;) {
-    const int32_t pos = __ldg(a.query_pos + qi);
+    const int32_t pos = position(a, qi);
     const TileRange ur = tile_range<kRows>(pos, a.window, a.n_sink);
     if (u >= q_start + (int64_t)ur.count * a.groups) {     // on to the next query (or past empty ones)
       q_start += (int64_t)ur.count * a.groups;
@@ -811,7 +813,12 @@ cudaError_t launch_gqa_attn(const uint16_t* q, const csa2_kv_cache& kv, const in
   a.q = q, a.out = out, a.lse = lse;
   const csa2_rows* views[4] = {&kv.k_codes, &kv.k_scales, &kv.v_codes, &kv.v_scales};
   a.one_map = 1;
+  int64_t limit = kMaxPositions;
   for (int i = 0; i < 4; ++i) {
+    const csa2_rows& v = *views[i];
+    const int64_t rows = v.page_table ? (int64_t)v.max_pages * v.page_rows
+                         : v.seq_rows > 0 ? std::min<int64_t>(v.seq_rows, v.n_rows) : v.n_rows;
+    limit = std::min(limit, rows);
     a.base[i] = static_cast<const uint8_t*>(views[i]->base);
     a.rb[i] = views[i]->row_bytes;
     a.map[i] = to_rowmap(*views[i]);
@@ -820,6 +827,7 @@ cudaError_t launch_gqa_attn(const uint16_t* q, const csa2_kv_cache& kv, const in
     for (int b = 6; b < 31; ++b)
       if (views[i]->page_table && views[i]->page_rows == 1 << b) a.page_shift[i] = b;
   }
+  a.limit = (int32_t)limit;
   a.seq_of_query = seq_of_query;
   a.query_pos = query_pos;
   a.nq = nq;

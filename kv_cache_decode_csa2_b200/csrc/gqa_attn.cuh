@@ -39,6 +39,7 @@ struct GqaArgs {
   const int32_t* seq_of_query;
   const int32_t* query_pos;
   int32_t nq, Hkv, G, window, n_sink;
+  int32_t limit;                   // positions from here on have no row in any sequence
   float scale_log2;
   int32_t n_cta;                   // CTAs of the main kernel
   int32_t q_tile;                  // queries per item of the block kernel (0: the split kernel, one query per item)
@@ -51,6 +52,15 @@ struct GqaArgs {
   float2* part_ml;                 // [2 n_cta][rows] (offset max in log2 units, sum)
   int32_t* status;
 };
+
+// Positions are held below this: 256 runs of a block then have fewer than 2^31 tiles.
+constexpr int64_t kMaxPositions = 1 << 29;
+// The position that query i works with: one past its plane's rows is taken as
+// the last there is (and reported by write_empties), so that neither the work
+// nor a neighbour's rows depend on it.
+__device__ __forceinline__ int32_t position(const GqaArgs& a, int64_t i) {
+  return min(__ldg(a.query_pos + i), a.limit - 1);
+}
 
 // The tiles of T rows that a query at position pos sees rows of: tile x starts
 // at row x T, from `sink` on `gap` rows later (the rows between the sinks and
@@ -141,14 +151,16 @@ __device__ __forceinline__ int64_t div_run(int64_t a, int64_t b) {
 // Joins the parts that CTAs left (gqa_attn.cu), of at most `items` items;
 // launched behind either kernel.
 cudaError_t launch_gqa_combine(const GqaArgs& a, int32_t D, int32_t run_heads, int64_t items, cudaStream_t st);
-// Outputs of this CTA's share of the queries that see no row, by all of its
-// N threads.
+// Outputs of this CTA's share of the queries that see no row, and the report
+// of those whose position is past every row, by all of its N threads.
 template <int N>
 __device__ __forceinline__ void write_empties(const GqaArgs& a, int32_t D) {
   const int64_t Hq = (int64_t)a.Hkv * a.G;
   for (int64_t base = blockIdx.x; base < a.nq; base += (int64_t)a.n_cta * N) {
     const int64_t mine = base + (int64_t)a.n_cta * threadIdx.x;
-    if (!__syncthreads_or(mine < a.nq && __ldg(a.query_pos + mine) < 0)) continue;
+    const int32_t p = mine < a.nq ? __ldg(a.query_pos + mine) : 0;
+    if (p >= a.limit) record_error(a.status, CSA2_ERR_INDEX_RANGE);
+    if (!__syncthreads_or(p < 0)) continue;
     for (int64_t q = base; q < a.nq && q < base + (int64_t)a.n_cta * N; q += a.n_cta) {
       if (__ldg(a.query_pos + q) >= 0) continue;
       for (int64_t i = threadIdx.x; i < Hq * D / 8; i += N)

@@ -203,7 +203,7 @@ __device__ int32_t list_runs(const GqaArgs& a, int32_t q0, int32_t n, Runs& r, i
   for (int base = 0; base < n; base += 32) {
     const int i = base + lane;
     const bool in = i < n;
-    const int32_t pos = in ? __ldg(a.query_pos + q0 + i) : -1;
+    const int32_t pos = in ? position(a, q0 + i) : -1;
     const int32_t seq = in ? (a.seq_of_query ? __ldg(a.seq_of_query + q0 + i) : q0 + i) : 0;
     int32_t prev = __shfl_up_sync(0xffffffffu, seq, 1);
     if (lane == 0) prev = carry;
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar->q_full);
       bool ok = true;
-      const int32_t pos = live ? __ldg(a.query_pos + it.q0 + qr) : -1;
+      const int32_t pos = live ? position(a, it.q0 + qr) : -1;
       const Seen mine = seen_rows(pos, a.window, a.n_sink);
       float mo = -INFINITY;
       float2 l = make_float2(0.f, 0.f);

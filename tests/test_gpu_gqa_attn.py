@@ -396,3 +396,38 @@ def test_two_handles_on_two_streams(group):
     for h, q64, out, lse, _ in calls:
         B.check_status(h.status)
         check_attention(cache, q64, seq, pos, out, lse)
+
+
+@pytest.mark.parametrize("window,n_sink", [(0, 0), (20, 3)])
+@pytest.mark.parametrize("group", [False, True])
+def test_positions_past_every_row_harm_no_neighbour(group, window, n_sink):
+    """Positions far past the rows (what an uninitialised tensor may hold) in
+    the same run as good ones, at a number of rows that is no multiple of a
+    page: reported, the others exact, and no longer a call than any."""
+    rng = np.random.default_rng(19)
+    cache = Cache(rng, 2, 192, 1, 64, paged=False, lens=[100, 100])
+    for x in cache.planes.values():
+        x[100:200] = x[192:292].copy()                # sequence 1 from row 100 on
+    cache.R = 100
+    cache.push()
+    seq, pos = [0] * 4 + [1] * 4, [98, 99, 100, 2 ** 31 - 1, 0x7F7F7F7F, 64, 10 ** 9, 99]
+    q, q64 = queries(rng, 8, 4, 64)
+    out = torch.zeros((8, 4, 64), dtype=torch.bfloat16, device=DEV)
+    lse = torch.zeros((8, 4), device=DEV)
+    call = B.GqaAttn(cache.c, q.to(DEV), torch.tensor(pos, dtype=torch.int32, device=DEV), out, lse=lse, window=window,
+                     n_sink=n_sink, seq_of_query=torch.tensor(seq, dtype=torch.int32, device=DEV), group_queries=group)
+    call.run()
+    assert int(call.status.item()) == 6
+    check_attention(cache, q64, seq, pos, out, lse, window, n_sink, only=[0, 1, 5, 7])
+
+
+@pytest.mark.parametrize("group", [False, True])
+def test_a_block_of_positions_past_every_row(group):
+    """A whole block of such positions, each its own sequence, one head per KV head."""
+    rng = np.random.default_rng(20)
+    cache = Cache(rng, 1, 64, 1, 64, paged=False)
+    q, _ = queries(rng, 300, 1, 64)
+    pos = torch.full((300,), 0x7F7F7F7F, dtype=torch.int32, device=DEV)
+    out = torch.zeros((300, 1, 64), dtype=torch.bfloat16, device=DEV)
+    st = B.csa2_gqa_attn_fp4(cache.c, q.to(DEV), pos, out, group_queries=group)
+    assert int(st.item()) == 6
