@@ -651,33 +651,9 @@ __global__ void __launch_bounds__(kCombWarps * 32, N == 8 ? 4 : 8) gqa_combine_k
     if (at < 0) continue;                                // W == kCombWarps: the block is one row
     // part p: the first CTA's last part, then each CTA's first
     auto part = [&](int p) { return (int64_t)(2 * (first + p) + (p == 0 ? 1 : 0)) * rows + row; };
-    float M = -INFINITY;
-    for (int p = wr * 32 + lane; p < parts; p += W * 32) M = fmaxf(M, __ldcg(&a.part_ml[part(p)]).x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (W > 1) {
-      if (lane == 0) m_s[warp] = M;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < W; ++w) M = fmaxf(M, m_s[w]);
-    }
-    float l = 0.f;
-    for (int p = wr * 32 + lane; p < parts; p += W * 32) {
-      const float2 ml = __ldcg(&a.part_ml[part(p)]);
-      // a part without a maximum saw only NaN, and its sum says so
-      const float f = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - M);
-      w_s[rr][p] = f;
-      l += f * ml.y;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (W > 1 && lane == 0) l_s[warp] = l;
-    block_sync();
-    float acc[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.f;
-    for (int p0 = wr; p0 < parts; p0 += N * W) {
-      float o[N][V];
+    // the first of a warp's parts, and of a lane's weights, on their way together
+    float o[N][V];
+    auto load_parts = [&](int p0) {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int p = p0 + i * W;
@@ -694,6 +670,37 @@ __global__ void __launch_bounds__(kCombWarps * 32, N == 8 ? 4 : 8) gqa_combine_k
           }
         }
       }
+    };
+    const int mine = wr * 32 + lane;
+    const float2 ml0 = mine < parts ? __ldcg(&a.part_ml[part(mine)]) : make_float2(-INFINITY, 0.f);
+    load_parts(wr);
+    float M = ml0.x;
+    for (int p = mine + W * 32; p < parts; p += W * 32) M = fmaxf(M, __ldcg(&a.part_ml[part(p)]).x);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    if (W > 1) {
+      if (lane == 0) m_s[warp] = M;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < W; ++w) M = fmaxf(M, m_s[w]);
+    }
+    float l = 0.f;
+    for (int p = mine; p < parts; p += W * 32) {
+      const float2 ml = p == mine ? ml0 : __ldcg(&a.part_ml[part(p)]);
+      // a part without a maximum saw only NaN, and its sum says so
+      const float f = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - M);
+      w_s[rr][p] = f;
+      l += f * ml.y;
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    if (W > 1 && lane == 0) l_s[warp] = l;
+    block_sync();
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int p0 = wr; p0 < parts; p0 += N * W) {
+      if (p0 != wr) load_parts(p0);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const int p = p0 + i * W;
