@@ -344,8 +344,8 @@ __device__ __forceinline__ void load_query(const GqaArgs& a, const uint16_t* q, 
 }
 
 // Sum over the block of one value per thread, and the sum of the threads
-// before this one.
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sh, int64_t* total) {
+// before this one; whether any thread has the flag.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sh, int64_t* total, bool flag, bool* any) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t s = v;
 #pragma unroll
@@ -354,7 +354,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sh, int64_t* t
     if (lane >= o) s += n;
   }
   if (lane == 31) sh[warp] = s;
-  __syncthreads();
+  *any = __syncthreads_or(flag);
   int64_t before = 0, all = 0;
 #pragma unroll
   for (int i = 0; i < kGqaWarps; ++i) {
@@ -394,9 +394,11 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
   {
     const int per = (a.nq + kGqaThreads - 1) / kGqaThreads;
     const int i0 = min(tid * per, a.nq), i1 = min(i0 + per, a.nq);
+    const bool empty = looks_empty<kGqaThreads, int32_t>(a);
     int64_t n = 0;
     for (int i = i0; i < i1; ++i) n += tile_range<kRows>(position(a, i), a.window, a.n_sink).count;
-    int64_t start = block_scan(n, scan_s, &total);
+    bool empties;
+    int64_t start = block_scan(n, scan_s, &total, empty, &empties);
     all = total * a.groups;
     run = max(div_run(all + a.n_cta - 1, a.n_cta), (int64_t)kMinRun);
     const int64_t u = (int64_t)blockIdx.x * run;
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
         start += c;
       }
     }
-    write_empties<kGqaThreads>(a, D);
+    if (empties) write_empties<kGqaThreads>(a, D);
     if (tid == 0) a.joints[blockIdx.x].i0 = -1;
     __syncthreads();
     if (u >= all) return;

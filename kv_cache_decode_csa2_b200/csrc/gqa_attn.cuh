@@ -56,7 +56,7 @@ struct GqaArgs {
 // Positions are held below this: 256 runs of a block then have fewer than 2^31 tiles.
 constexpr int64_t kMaxPositions = 1 << 29;
 // The position that query i works with: one past its plane's rows is taken as
-// the last there is (and reported by write_empties), so that neither the work
+// the last there is (and reported by looks_empty), so that neither the work
 // nor a neighbour's rows depend on it.
 __device__ __forceinline__ int32_t position(const GqaArgs& a, int64_t i) {
   return min(__ldg(a.query_pos + i), a.limit - 1);
@@ -151,23 +151,33 @@ __device__ __forceinline__ int64_t div_run(int64_t a, int64_t b) {
 // Joins the parts that CTAs left (gqa_attn.cu), of at most `items` items;
 // launched behind either kernel.
 cudaError_t launch_gqa_combine(const GqaArgs& a, int32_t D, int32_t run_heads, int64_t items, cudaStream_t st);
-// Outputs of this CTA's share of the queries that see no row, and the report
-// of those whose position is past every row, by all of its N threads.
+// The queries of a CTA: blockIdx.x, n_cta queries on, ...  Thread i looks at
+// the i-th: reports a position past every row and says whether one sees none.
+// (Read where the kernel starts; the answers meet at a barrier it has anyway.)
+// With a 64-bit index I the block kernel behind it comes out 2% faster (windowed
+// chunk of 4,096 queries 264 for 269 us), with 32 bits the split kernel's
+// start 0.7 us shorter (one query over 4,096 rows 12.9 for 13.6 us).
+template <int N, typename I>
+__device__ __forceinline__ bool looks_empty(const GqaArgs& a) {
+  bool empty = false;
+#pragma unroll(sizeof(I) == 4 ? 1 : 4)
+  for (I q = blockIdx.x + (I)a.n_cta * threadIdx.x; q < a.nq; q += (I)a.n_cta * N) {
+    const int32_t p = __ldg(a.query_pos + q);
+    if (p >= a.limit) record_error(a.status, CSA2_ERR_INDEX_RANGE);
+    empty = empty || p < 0;
+  }
+  return empty;
+}
+// The outputs of those that see no row, by all N threads.
 template <int N>
 __device__ __forceinline__ void write_empties(const GqaArgs& a, int32_t D) {
   const int64_t Hq = (int64_t)a.Hkv * a.G;
-  for (int64_t base = blockIdx.x; base < a.nq; base += (int64_t)a.n_cta * N) {
-    const int64_t mine = base + (int64_t)a.n_cta * threadIdx.x;
-    const int32_t p = mine < a.nq ? __ldg(a.query_pos + mine) : 0;
-    if (p >= a.limit) record_error(a.status, CSA2_ERR_INDEX_RANGE);
-    if (!__syncthreads_or(p < 0)) continue;
-    for (int64_t q = base; q < a.nq && q < base + (int64_t)a.n_cta * N; q += a.n_cta) {
-      if (__ldg(a.query_pos + q) >= 0) continue;
-      for (int64_t i = threadIdx.x; i < Hq * D / 8; i += N)
-        reinterpret_cast<uint4*>(a.out + q * Hq * D)[i] = make_uint4(0, 0, 0, 0);
-      if (a.lse)
-        for (int64_t i = threadIdx.x; i < Hq; i += N) a.lse[q * Hq + i] = -INFINITY;
-    }
+  for (int64_t q = blockIdx.x; q < a.nq; q += a.n_cta) {
+    if (__ldg(a.query_pos + q) >= 0) continue;
+    for (int64_t i = threadIdx.x; i < Hq * D / 8; i += N)
+      reinterpret_cast<uint4*>(a.out + q * Hq * D)[i] = make_uint4(0, 0, 0, 0);
+    if (a.lse)
+      for (int64_t i = threadIdx.x; i < Hq; i += N) a.lse[q * Hq + i] = -INFINITY;
   }
 }
 // Blocks of queries on the tensor cores (gqa_block.cu): the fields of a that

@@ -265,6 +265,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
   pdl_wait();      // launched while the grid before it drains
   pdl_trigger();
 
+  const bool empty = looks_empty<kBlockThreads, int64_t>(a);
+
   // ---- prologue: barriers, TMEM, and where this CTA's run of tiles starts
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
     }
   }
   tc_fence_before();
-  __syncthreads();
+  const bool empties = __syncthreads_or(empty);
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   int64_t all, run;
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       }
       start += counts[b];
     }
-    write_empties<kBlockThreads>(a, D);
+    if (empties) write_empties<kBlockThreads>(a, D);
     if (tid == 0) a.joints[blockIdx.x].i0 = -1;
     __syncthreads();
   }
