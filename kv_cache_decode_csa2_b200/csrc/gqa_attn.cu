@@ -20,8 +20,8 @@
 // of bf16's 8 bits for values down to 2^-28 of the row's largest.
 //
 // Measured on 64 query and 8 KV heads, D = 128: one query over 1,048,576 rows
-// 292 us (3.9 TB/s, 0.60 of the copy rate), 32 queries over 572,000 rows
-// 167 us (3.7 TB/s).  What bounds it is the expansion of the codes: the
+// 280 to 292 us (3.9 to 4.1 TB/s, 0.60 of the copy rate), 32 queries over
+// 572,000 rows 166 us (3.7 TB/s).  What bounds it is the expansion of the codes: the
 // conversions, byte permutes and f16 products issue at half rate and, with
 // the rest, fill 62% of the issue slots at four warps per scheduler.  Against
 // what stood when each was tried, 16-row tiles took 383 us for 326, V of a
@@ -69,8 +69,8 @@ constexpr int kRows = 32;
 constexpr int kStages = 3;
 static_assert(kRows == 32 && kStages == 3, "a lane per row of scales, written a turn before they are read");
 // Tiles a CTA takes at least: one each makes as many parts as there are tiles
-// to join.  A query over 4,096 rows takes 19.1, 16.8, 17.3, 18.8, 21.2 us with
-// 1, 2, 3, 4, 6.
+// to join.  A query over 4,096 rows took 19.1, 16.8, 17.3, 18.8, 21.2 us with
+// 1, 2, 3, 4, 6 (12.9 us by now).
 constexpr int kMinRun = 2;
 template <int D>
 struct GqaRing {
