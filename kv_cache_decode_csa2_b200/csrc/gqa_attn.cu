@@ -577,7 +577,7 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
             for (int j = 0; j < D / 32; ++j)
               reinterpret_cast<float4*>(a.part_o + at * D + g * (D / 8))[j] =
                   make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            if (g == 0) a.part_ml[at] = make_float2(st.mo[n][e], st.l[n][e]);
+            if (g == 0) a.part_ml[at] = make_float2(st.mo[n][e] + kOffset, st.l[n][e]);
           }
         }
     }
@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(kCombWarps * 32, N == 8 ? 4 : 8) gqa_combine_k
         const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
         dst[i] = *reinterpret_cast<const uint32_t*>(&b);
       }
-      if (lane == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
+      if (lane == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (M + (log2f(l) - kOffset)) * 0.69314718055994531f;
     }
     block_sync();                                      // shared memory is free for the next
   }

@@ -769,7 +769,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       bool ok = true;
       const int32_t pos = live ? position(a, it.q0 + qr) : -1;
       const Seen mine = seen_rows(pos, a.window, a.n_sink);
-      float mo = -INFINITY;
+      float mx = -INFINITY;                      // the row's reference
+      float mul = qs, sub = 0.f;                 // a weight's exponent is x mul - sub of what stands in a column
       float2 l = make_float2(0.f, 0.f);
       const bool idle = !__any_sync(0xffffffffu, live);      // no row of this warp is anyone's
       for (int32_t x = x0; x < c1; x += step, ++n_s) {
@@ -789,10 +790,12 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
           return below(w.hi + 1 - 32 * y) & (~below(w.lo - 32 * y) | below(w.sk - 32 * y));
         };
         // The weights, 32 columns at a time, over the logits' columns.  The
-        // maximum moves only when a logit exceeds it by kLazy: O, the sum and
-        // the weights of the tile already stored are then scaled, and these
-        // columns, taken on trust, are taken again.  (One rolled loop: the
-        // code of the roles has to stay in the instruction caches together.)
+        // reference moves only when a logit exceeds it by kLazy (past kFine in
+        // every tile, to the largest of the columns left): O, the sum and the
+        // weights of the tile already stored are then scaled, and these
+        // columns, taken on trust, are taken again, once.  (One rolled loop:
+        // the code of the roles has to stay in the instruction caches together.)
+        float limit = fabsf(mx) <= kFine ? kOffset + kLazy : -INFINITY;
 #pragma unroll 1
         for (int y = idle ? 4 : 0; y < 4;) {
           uint32_t s[32];
@@ -804,11 +807,10 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
             for (int c = 0; c < 32; ++c)
               if (!((bits >> c) & 1u)) s[c] = 0xFF800000u;
           }
-          const float sub = mo == -INFINITY ? 0.f : mo;
           float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            const float2 v = fma2(s[2 * c], s[2 * c + 1], qs, -sub);
+            const float2 v = fma2(s[2 * c], s[2 * c + 1], mul, -sub);
             s[2 * c] = __float_as_uint(v.x), s[2 * c + 1] = __float_as_uint(v.y);
             top[c & 1] = max3(top[c & 1], v.x, v.y);
           }
@@ -822,16 +824,48 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
             p[c] = *reinterpret_cast<const uint32_t*>(&hh);
           }
           const float most = fmaxf(top[0], top[1]);
-          if (!__any_sync(0xffffffffu, most > (mo == -INFINITY ? -INFINITY : kOffset + kLazy))) {
+          if (!__any_sync(0xffffffffu, most > limit)) {
             l.x += add.x, l.y += add.y;
             tmem_st16(s_t + 16 * y, p);
+            if (limit == INFINITY) limit = mx == -INFINITY ? -INFINITY : kOffset + kLazy;
             ++y;
             continue;
           }
           // a whole number: weights already rounded are scaled exactly
-          const float m_new = fmaxf(mo, floorf(most + sub) - kOffset);
-          const float f = mo == -INFINITY ? 0.f : ex2(mo - m_new);
-          mo = m_new;
+          const bool done = past_fine(mx) && limit > -INFINITY;      // an earlier turn of this tile did what follows
+          float m_new = done ? mx : fmaxf(mx, floorf(most + sub));
+          const bool far = !done && (past_fine(mx) || past_fine(m_new));
+          if (__any_sync(0xffffffffu, far)) {
+            // these rows' logits, each rounded once: the largest, then exponents in their place
+            float high = -INFINITY;
+#pragma unroll 1
+            for (int z = 2 * y; z < 8; ++z) {
+              const uint32_t bits = full ? ~0u : see(z >> 1) >> (16 * (z & 1));
+              uint32_t b[16];
+              tmem_ld16(s_t + 16 * z, b);
+              tmem_wait_ld16(b);
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                if ((bits >> c) & 1u) high = fmaxf(high, __fmul_rn(__uint_as_float(b[c]), qs));
+            }
+            if (far) m_new = fmaxf(mx, floorf(high));
+            const bool put = far && past_fine(m_new);
+#pragma unroll 1
+            for (int z = 2 * y; z < 8; ++z) {
+              uint32_t b[16];
+              tmem_ld16(s_t + 16 * z, b);
+              tmem_wait_ld16(b);
+#pragma unroll
+              for (int c = 0; c < 16; ++c)
+                if (put) b[c] = __float_as_uint(far_exponent(__uint_as_float(b[c]), qs, m_new));
+              tmem_st16(s_t + 16 * z, b);
+            }
+          }
+          const float f = mx == -INFINITY ? 0.f : ex2(mx - m_new);
+          mx = m_new;
+          mul = past_fine(mx) ? 1.f : qs;
+          sub = fabsf(mx) <= kFine ? mx - kOffset : 0.f;
+          limit = INFINITY;                      // taken now, whatever comes
           l.x *= f, l.y *= f;
           tmem_wait_st();                        // the weights before are in place
 #pragma unroll 1
@@ -891,19 +925,19 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
               reinterpret_cast<uint4*>(o_s)[(4 * y + c) * 128 + r] =
                   some ? make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]) : make_uint4(0, 0, 0, 0);
           }
-          join_s[r] = make_float2(mo, sum);
+          join_s[r] = make_float2(mx, sum);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar->stored);
         } else {
           ok = __all_sync(0xffffffffu, block_wait(&bar->stored, n_pair & 1, abort_flag));
           if (!ok) break;
           const float2 ml = join_s[r];
-          const float top = fmaxf(mo, ml.x);
+          const float top = fmaxf(mx, ml.x);
           // a side without a maximum saw nothing, or only NaN: its sum is 0 or NaN
-          const float f0 = mo == -INFINITY ? (sum != sum ? sum : 0.f) : ex2(mo - top);
+          const float f0 = mx == -INFINITY ? (sum != sum ? sum : 0.f) : ex2(mx - top);
           scale = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - top);
           sum = sum * f0 + ml.y * scale;
-          mo = top;
+          mx = top;
           l.x = f0;                              // O of the first height is scaled by it below
         }
       }
@@ -948,8 +982,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
           }
         }
         if (live && slot < 0 && a.lse)
-          a.lse[out_row] = sum == 0.f ? -INFINITY : (mo + log2f(sum)) * 0.69314718055994531f;
-        if (live && slot >= 0) a.part_ml[part] = make_float2(mo, sum);
+          a.lse[out_row] = sum == 0.f ? -INFINITY : (mx + (log2f(sum) - kOffset)) * 0.69314718055994531f;
+        if (live && slot >= 0) a.part_ml[part] = make_float2(mx, sum);
       }
       __syncwarp();
       if (pair) {                                // the space of Q is free when the first height has read it

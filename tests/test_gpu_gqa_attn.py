@@ -431,3 +431,44 @@ def test_a_block_of_positions_past_every_row(group):
     out = torch.zeros((300, 1, 64), dtype=torch.bfloat16, device=DEV)
     st = B.csa2_gqa_attn_fp4(cache.c, q.to(DEV), pos, out, group_queries=group)
     assert int(st.item()) == 6
+
+
+@pytest.mark.parametrize("group", [True])
+@pytest.mark.parametrize("nq,Hq", [(6, 4), (40, 8)])
+def test_logits_of_any_size(nq, Hq, group):
+    """Queries of neighbouring rows whose logits lie between 2^0 and 2^100 (a
+    diverged layer, a buffer nobody wrote), in every other head all of them
+    negative.  Where one row's logit is ahead of every other by more than twice
+    their error and 40 more, its weight is 1 to 300 e^-40 < 2^-49: the output
+    is its values, rounded as a weight of f16 and to bf16, and the lse its
+    logit.  Everywhere the output is an average."""
+    rng = np.random.default_rng(21)
+    cache = Cache(rng, 1, 300, 1, 128, paged=False)
+    u = np.sign(rng.standard_normal(128))
+    c, sc = O.fp4_quantize(u + 0.5 * rng.standard_normal((300, 128)))
+    cache.planes["k_codes"][:300], cache.planes["k_scales"][:300] = c, sc
+    cache.push()
+    sizes = [4, 18, 27, 0, 22, 100, 3, 28, 20, 2, 33, 26, 60]
+    e = np.array([sizes[i % len(sizes)] for i in range(nq)])
+    q = rng.standard_normal((nq, Hq, 128))
+    q[:, 1::2] = -u * np.abs(q[:, 1::2])
+    q, q64 = bf16(q * 2.0 ** e[:, None, None])
+    seq, pos = [0] * nq, list(range(300 - nq, 300))
+    out, lse = attend(cache, q, seq, pos, group_queries=group)
+    check_attention(cache, q64, seq, pos, out, lse, only=np.flatnonzero(e < 8))
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    certain = 0
+    for i in np.flatnonzero(e > 8):
+        k, v = (cache.values(x, 0, np.arange(pos[i] + 1))[:, 0] for x in "kv")
+        assert (np.abs(out[i]) <= np.abs(v).max(0) * (1 + 2.0 ** -7)).all()
+        logit = q64[i] @ k.T / np.sqrt(128)
+        assert (logit[1::2] < 0).all()
+        d = (128 + 4) * 2.0 ** -24 * (np.abs(q64[i]) @ np.abs(k).T / np.sqrt(128)).max(1)
+        order = np.argsort(logit, 1)
+        for h in range(Hq):
+            first, second = order[h, -1], order[h, -2]
+            if logit[h, first] - logit[h, second] > 2 * d[h] + 40:
+                certain += 1
+                assert (np.abs(out[i, h] - v[first]) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(v[first]) + 2.0 ** -40).all()
+            assert abs(lse[i, h] - logit[h, first]) <= d[h] + np.log(300) + 2.0 ** -22 * abs(logit[h, first])
+    assert certain > 0.9 * (e > 8).sum() * Hq
