@@ -29,10 +29,10 @@
 // for 292, and 80 registers for a third CTA per SM 429 for 292 (spills).
 //
 // The maximum is lazy: m moves only when a logit exceeds it by 5 (log2), and
-// weights are 2^(s - m + 10) <= 2^15.  A row's largest is then at least 2^10,
-// so in f16 a weight keeps 11 bits down to 2^-24 of the largest and vanishes
-// only below 2^-35: a million rows of small weights beside one large sink
-// still count.  Sums are fp32 of the unrounded weights.
+// weights are 2^(s - m + 10) <= 2^15 (logits past 2^20: gqa_attn.cuh).  A row's
+// largest is then at least 2^10, so in f16 a weight keeps 11 bits down to 2^-24
+// of the largest and vanishes only below 2^-35: a million rows of small weights
+// beside one large sink still count.  Sums are fp32 of the unrounded weights.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -186,7 +186,7 @@ __device__ __forceinline__ void lds_words(const uint8_t* p, uint32_t (&w)[N]) {
 template <int D, int NT>
 struct GqaState {
   float o[NT][D / 16][4];     // O^T: dims g D/8 + 2j (+ 1), heads 2t and 2t + 1
-  float mo[NT][2];            // maximum in use minus kOffset, log2 units (-inf: no row yet)
+  float mo[NT][2];            // reference (-inf: no row yet)
   float l[NT][2];             // this lane's part of the sum of weights
 };
 
@@ -222,7 +222,7 @@ __device__ __forceinline__ void tile_step(GqaState<D, NT>& st, const uint8_t* st
       }
     }
   }
-  // x = the logit above the maximum in use, plus kOffset
+  // x = the logit above the reference
   bool see[2 * H];
 #pragma unroll
   for (int i = 0; i < 2 * H; ++i) see[i] = true;
@@ -241,7 +241,11 @@ __device__ __forceinline__ void tile_step(GqaState<D, NT>& st, const uint8_t* st
         x[h][n][i] = see[2 * h + (i >> 1)] ? fmaf(s[h][n][i], qs[n][i & 1], -st.mo[n][i & 1]) : -INFINITY;
         top = fmaxf(top, x[h][n][i]);
       }
-  if (__any_sync(0xffffffffu, top > kOffset + kLazy)) {
+  // past kFine in every tile, whose x are then taken from rounded logits
+  bool move = top > kOffset + kLazy;
+#pragma unroll
+  for (int n = 0; n < NT; ++n) move = move || past_fine(st.mo[n][0]) || past_fine(st.mo[n][1]);
+  if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float f[2];
@@ -249,16 +253,16 @@ __device__ __forceinline__ void tile_step(GqaState<D, NT>& st, const uint8_t* st
       for (int e = 0; e < 2; ++e) {
         float m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 2 * H; ++i) m = see[i] ? fmaxf(m, s[i >> 1][n][2 * (i & 1) + e] * qs[n][e]) : m;
+        for (int i = 0; i < 2 * H; ++i) m = see[i] ? fmaxf(m, __fmul_rn(s[i >> 1][n][2 * (i & 1) + e], qs[n][e])) : m;
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float mo = fmaxf(st.mo[n][e], m - kOffset);
+        const float mo = fmaxf(st.mo[n][e], reference(m));
         f[e] = st.mo[n][e] == -INFINITY ? 0.f : ex2(st.mo[n][e] - mo);
         st.mo[n][e] = mo;
         st.l[n][e] *= f[e];
 #pragma unroll
         for (int i = 0; i < 2 * H; ++i)
-          x[i >> 1][n][2 * (i & 1) + e] = see[i] ? fmaf(s[i >> 1][n][2 * (i & 1) + e], qs[n][e], -mo) : -INFINITY;
+          x[i >> 1][n][2 * (i & 1) + e] = see[i] ? exponent(s[i >> 1][n][2 * (i & 1) + e], qs[n][e], mo) : -INFINITY;
       }
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
@@ -577,7 +581,7 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
             for (int j = 0; j < D / 32; ++j)
               reinterpret_cast<float4*>(a.part_o + at * D + g * (D / 8))[j] =
                   make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-            if (g == 0) a.part_ml[at] = make_float2(st.mo[n][e] + kOffset, st.l[n][e]);
+            if (g == 0) a.part_ml[at] = make_float2(st.mo[n][e], st.l[n][e]);
           }
         }
     }
@@ -733,7 +737,7 @@ __global__ void __launch_bounds__(kCombWarps * 32, N == 8 ? 4 : 8) gqa_combine_k
         const __nv_bfloat162 b = __floats2bfloat162_rn(acc[2 * i] * inv, acc[2 * i + 1] * inv);
         dst[i] = *reinterpret_cast<const uint32_t*>(&b);
       }
-      if (lane == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (M + (log2f(l) - kOffset)) * 0.69314718055994531f;
+      if (lane == 0 && a.lse) a.lse[at] = l == 0.f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
     }
     block_sync();                                      // shared memory is free for the next
   }

@@ -49,7 +49,7 @@ struct GqaArgs {
   int32_t groups;                  // items per query or block: ceil(vh / per_cta)
   GqaJoint* joints;                // [n_cta] what each CTA shares with the one before it
   float* part_o;                   // [2 n_cta][rows][D] unnormalised O of a part
-  float2* part_ml;                 // [2 n_cta][rows] (reference in log2 units, sum of weights)
+  float2* part_ml;                 // [2 n_cta][rows] (reference, sum of weights)
   int32_t* status;
 };
 
@@ -90,25 +90,28 @@ __device__ __forceinline__ Seen seen_rows(int32_t pos, int32_t window, int32_t n
   return Seen{pos, window > 0 && pos >= window ? pos - window + 1 : 0, n_sink};
 }
 
-// Weights are 2^(L - m + kOffset): L the logit in log2 units, m the row's
-// reference, a whole number that is at most the largest L so far and that an L
-// may exceed by kLazy before it moves.
+// Weights are 2^(L - r): L the logit in log2 units, r the row's reference,
+// kOffset below the largest L so far (a whole number), until an L is more than
+// kLazy above that.
 //
-// Up to kFine, m - kOffset is exact and L - (m - kOffset) one fused
-// multiply-add of the product s and its scale; rounding an L of that size moves
-// it by less than 2^-3, so that the largest weight is 2^10 to 2^15, to within
-// that.  Past it this falls apart:
-// from 2^27 on the offset is lost beside m, and a fused product differs from
-// the rounded one by more than the offset, so that the largest exponent may be
-// anything (an endless search for the maximum, infinite weights).  There L is
-// rounded first, as m was; L - m is then exact for what counts, and 0 to 1 for
-// the largest, whatever its magnitude.
+// While r is up to kFine, L - r is one fused multiply-add of a product of q and
+// k with its scale; an L rounded by itself is off by less than 2^-3 there.  Past
+// that a fused product differs from the rounded one by more and more, from 2^27
+// on by more than the offset, which is then lost beside L as well: the largest
+// exponent could be anything (infinite weights, an endless search for the
+// maximum).  So past kFine every L is rounded first, which makes L - r exact
+// for what counts, and past kExact, where r cannot hold the offset, it goes
+// without (a logit's own error is 1 there, and a weight below 2^-25 nothing).
 constexpr float kLazy = 5.f;
 constexpr float kOffset = 10.f;
-constexpr float kFine = 1 << 20;
-__device__ __forceinline__ bool past_fine(float m) { return fabsf(m) > kFine && m != -INFINITY; }   // -inf: no row yet
-__device__ __forceinline__ float far_exponent(float s, float scale, float m) {
-  return __fadd_rn(__fsub_rn(__fmul_rn(s, scale), m), kOffset);
+constexpr float kFine = 1 << 20, kExact = 1 << 24;
+__device__ __forceinline__ float reference(float largest) {       // -inf: no row yet
+  const float m = floorf(largest);
+  return fabsf(m) <= kExact ? m - kOffset : m;
+}
+__device__ __forceinline__ bool past_fine(float r) { return fabsf(r) > kFine && r != -INFINITY; }
+__device__ __forceinline__ float exponent(float s, float scale, float r) {
+  return past_fine(r) ? __fsub_rn(__fmul_rn(s, scale), r) : fmaf(s, scale, -r);
 }
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {

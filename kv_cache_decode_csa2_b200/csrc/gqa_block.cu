@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       bool ok = true;
       const int32_t pos = live ? position(a, it.q0 + qr) : -1;
       const Seen mine = seen_rows(pos, a.window, a.n_sink);
-      float mx = -INFINITY;                      // the row's reference
+      float mo = -INFINITY;                      // the row's reference
       float mul = qs, sub = 0.f;                 // a weight's exponent is x mul - sub of what stands in a column
       float2 l = make_float2(0.f, 0.f);
       const bool idle = !__any_sync(0xffffffffu, live);      // no row of this warp is anyone's
@@ -795,7 +795,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         // weights of the tile already stored are then scaled, and these
         // columns, taken on trust, are taken again, once.  (One rolled loop:
         // the code of the roles has to stay in the instruction caches together.)
-        float limit = fabsf(mx) <= kFine ? kOffset + kLazy : -INFINITY;
+        mul = qs;
+        float limit = fabsf(mo) <= kFine ? kOffset + kLazy : -INFINITY;
 #pragma unroll 1
         for (int y = idle ? 4 : 0; y < 4;) {
           uint32_t s[32];
@@ -827,16 +828,16 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
           if (!__any_sync(0xffffffffu, most > limit)) {
             l.x += add.x, l.y += add.y;
             tmem_st16(s_t + 16 * y, p);
-            if (limit == INFINITY) limit = mx == -INFINITY ? -INFINITY : kOffset + kLazy;
+            if (limit == INFINITY) limit = mo == -INFINITY ? -INFINITY : kOffset + kLazy;
             ++y;
             continue;
           }
           // a whole number: weights already rounded are scaled exactly
-          const bool done = past_fine(mx) && limit > -INFINITY;      // an earlier turn of this tile did what follows
-          float m_new = done ? mx : fmaxf(mx, floorf(most + sub));
-          const bool far = !done && (past_fine(mx) || past_fine(m_new));
+          const bool done = past_fine(mo) && limit > -INFINITY;      // an earlier turn of this tile did what follows
+          float m_new = done ? mo : fmaxf(mo, reference(most + sub));
+          const bool far = !done && (past_fine(mo) || past_fine(m_new));
           if (__any_sync(0xffffffffu, far)) {
-            // these rows' logits, each rounded once: the largest, then exponents in their place
+            // these rows' logits, each rounded once, in the products' place, and the largest
             float high = -INFINITY;
 #pragma unroll 1
             for (int z = 2 * y; z < 8; ++z) {
@@ -845,26 +846,19 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
               tmem_ld16(s_t + 16 * z, b);
               tmem_wait_ld16(b);
 #pragma unroll
-              for (int c = 0; c < 16; ++c)
-                if ((bits >> c) & 1u) high = fmaxf(high, __fmul_rn(__uint_as_float(b[c]), qs));
-            }
-            if (far) m_new = fmaxf(mx, floorf(high));
-            const bool put = far && past_fine(m_new);
-#pragma unroll 1
-            for (int z = 2 * y; z < 8; ++z) {
-              uint32_t b[16];
-              tmem_ld16(s_t + 16 * z, b);
-              tmem_wait_ld16(b);
-#pragma unroll
-              for (int c = 0; c < 16; ++c)
-                if (put) b[c] = __float_as_uint(far_exponent(__uint_as_float(b[c]), qs, m_new));
+              for (int c = 0; c < 16; ++c) {
+                const float v = __fmul_rn(__uint_as_float(b[c]), qs);
+                if ((bits >> c) & 1u) high = fmaxf(high, v);
+                if (far) b[c] = __float_as_uint(v);
+              }
               tmem_st16(s_t + 16 * z, b);
             }
+            if (far) m_new = fmaxf(mo, reference(high));
           }
-          const float f = mx == -INFINITY ? 0.f : ex2(mx - m_new);
-          mx = m_new;
-          mul = past_fine(mx) ? 1.f : qs;
-          sub = fabsf(mx) <= kFine ? mx - kOffset : 0.f;
+          const float f = mo == -INFINITY ? 0.f : ex2(mo - m_new);
+          mo = m_new;
+          if (far) mul = 1.f;
+          sub = mo == -INFINITY ? 0.f : mo;
           limit = INFINITY;                      // taken now, whatever comes
           l.x *= f, l.y *= f;
           tmem_wait_st();                        // the weights before are in place
@@ -925,19 +919,19 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
               reinterpret_cast<uint4*>(o_s)[(4 * y + c) * 128 + r] =
                   some ? make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]) : make_uint4(0, 0, 0, 0);
           }
-          join_s[r] = make_float2(mx, sum);
+          join_s[r] = make_float2(mo, sum);
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar->stored);
         } else {
           ok = __all_sync(0xffffffffu, block_wait(&bar->stored, n_pair & 1, abort_flag));
           if (!ok) break;
           const float2 ml = join_s[r];
-          const float top = fmaxf(mx, ml.x);
+          const float top = fmaxf(mo, ml.x);
           // a side without a maximum saw nothing, or only NaN: its sum is 0 or NaN
-          const float f0 = mx == -INFINITY ? (sum != sum ? sum : 0.f) : ex2(mx - top);
+          const float f0 = mo == -INFINITY ? (sum != sum ? sum : 0.f) : ex2(mo - top);
           scale = ml.x == -INFINITY ? (ml.y != ml.y ? ml.y : 0.f) : ex2(ml.x - top);
           sum = sum * f0 + ml.y * scale;
-          mx = top;
+          mo = top;
           l.x = f0;                              // O of the first height is scaled by it below
         }
       }
@@ -982,8 +976,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
           }
         }
         if (live && slot < 0 && a.lse)
-          a.lse[out_row] = sum == 0.f ? -INFINITY : (mx + (log2f(sum) - kOffset)) * 0.69314718055994531f;
-        if (live && slot >= 0) a.part_ml[part] = make_float2(mx, sum);
+          a.lse[out_row] = sum == 0.f ? -INFINITY : (mo + log2f(sum)) * 0.69314718055994531f;
+        if (live && slot >= 0) a.part_ml[part] = make_float2(mo, sum);
       }
       __syncwarp();
       if (pair) {                                // the space of Q is free when the first height has read it

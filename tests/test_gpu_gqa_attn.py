@@ -433,7 +433,7 @@ def test_a_block_of_positions_past_every_row(group):
     assert int(st.item()) == 6
 
 
-@pytest.mark.parametrize("group", [True])
+@pytest.mark.parametrize("group", [False, True])
 @pytest.mark.parametrize("nq,Hq", [(6, 4), (40, 8)])
 def test_logits_of_any_size(nq, Hq, group):
     """Queries of neighbouring rows whose logits lie between 2^0 and 2^100 (a
