@@ -423,7 +423,8 @@ class _Call:
     """A marshalled C call: run() is one call into the library (and can be
     captured in a CUDA graph).  It keeps every tensor it was made with."""
 
-    scratch: tuple = ()      # tensors made here: held back from reuse while another stream works with them
+    scratch: tuple = ()      # tensors made here, on the stream that was current then: `streams` holds those that
+                             # know of them, so that they are not given back while another still works with them
 
     def _make(self, name, device, args, keep, status):
         if device.type != "cuda":
@@ -439,6 +440,10 @@ class _Call:
         _dev(self.status, torch.int32, "status")
         if self.status.device != device:
             raise ValueError(f"{name}: status is on {self.status.device}, the cache on {device}")
+        self.streams = {torch._C._cuda_getCurrentRawStream(device.index)}
+        self.made = None
+        if self.scratch and not torch.cuda.is_current_stream_capturing():
+            self.made = torch.cuda.current_stream(device).record_event()
         self.fn = getattr(lib(), name)
         # converted once: ctypes then passes the same objects every time
         self.args = tuple(t(x) if t in (_P, _I32, _I64, _SZ, _F) else x
@@ -452,9 +457,22 @@ class _Call:
             raw = torch._C._cuda_getCurrentRawStream(self.device.index)
         else:
             raw = stream.cuda_stream
-            for t in self.scratch:
-                t.record_stream(stream)
+        if raw not in self.streams:
+            self._used_on(torch.cuda.current_stream(self.device) if stream is None else stream)
         _check(self.fn(*self.args, raw), self.name)
+
+    def _used_on(self, stream) -> None:
+        """A stream other than the scratch's own: it waits until that is made, and the allocator waits for it."""
+        if not self.scratch:
+            return
+        for t in self.scratch:
+            t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            capturing = torch.cuda.is_current_stream_capturing()
+        if not capturing:        # (a capture cannot wait for work outside it, nor work outside for a capture)
+            if self.made is not None:
+                stream.wait_event(self.made)
+            self.streams.add(stream.cuda_stream)
 
 
 def _heads(t, n_heads, D, dtype, n, name) -> int:

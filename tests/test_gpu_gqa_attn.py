@@ -472,3 +472,31 @@ def test_logits_of_any_size(nq, Hq, group):
                 assert (np.abs(out[i, h] - v[first]) <= (2.0 ** -8 + 2.0 ** -10) * np.abs(v[first]) + 2.0 ** -40).all()
             assert abs(lse[i, h] - logit[h, first]) <= d[h] + np.log(300) + 2.0 ** -22 * abs(logit[h, first])
     assert certain > 0.9 * (e > 8).sum() * Hq
+
+
+@pytest.mark.parametrize("group", [False, True])
+def test_a_handle_dropped_while_its_stream_works(group):
+    """Made on one stream, run with another as the current one, dropped: its
+    workspace is not handed out before the other stream is through."""
+    rng = np.random.default_rng(22)
+    cache = Cache(rng, 1, 3000, 2, 128, paged=True)
+    pos = [2996, 2997, 2998, 2999]
+    q, q64 = queries(rng, 4, 16, 128)
+    out, lse = torch.empty((4, 16, 128), dtype=torch.bfloat16, device=DEV), torch.empty((4, 16), device=DEV)
+    status = B.new_status(DEV)
+    qd, p = q.to(DEV), torch.tensor(pos, dtype=torch.int32, device=DEV)
+    seq = torch.zeros(4, dtype=torch.int32, device=DEV)
+    call = B.GqaAttn(cache.c, qd, p, out, seq_of_query=seq, lse=lse, group_queries=group, status=status)
+    at, n = call.keep["ws"].data_ptr(), call.keep["ws"].numel()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)             # about 10 ms
+        call.run()
+    del call
+    again = torch.empty(n, dtype=torch.uint8, device=DEV)
+    assert again.data_ptr() != at
+    again.fill_(0xFF)
+    torch.cuda.synchronize()
+    B.check_status(status)
+    check_attention(cache, q64, [0] * 4, pos, out, lse)

@@ -152,6 +152,67 @@ def test_the_binding_refuses_before_the_library():
     assert B._heads(torch.zeros(1, 2, 64), 2, 64, torch.float32, 1, "k") == 128
 
 
+class _Stream:
+    def __init__(self, raw):
+        self.cuda_stream, self.waited = raw, []
+
+    def wait_event(self, event):
+        self.waited.append(event)
+
+
+class _Tensor:
+    def __init__(self):
+        self.streams = []
+
+    def record_stream(self, stream):
+        self.streams.append(stream.cuda_stream)
+
+
+@pytest.mark.parametrize("given", [False, True])
+def test_scratch_is_held_for_every_stream_that_works_with_it(monkeypatch, given):
+    """A handle made on stream 7 and run on 8 and 9, as the current stream or
+    by name: its scratch is recorded on both before each first launch, which
+    waits for it to be made; a capturing stream cannot wait."""
+    current, capturing = [_Stream(7)], []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: current[-1].cuda_stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: current[-1])
+
+    class using:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            current.append(self.s)
+
+        def __exit__(self, *a):
+            current.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", using)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: current[-1].cuda_stream in capturing)
+    launched = []
+    t = _Tensor()
+    call = object.__new__(B.GqaAttn)
+    call.name, call.device, call.args, call.scratch = "fake", torch.device("cuda:0"), (), (t,)
+    call.streams, call.made = {7}, "made"
+    call.fn = lambda raw: launched.append((raw, list(t.streams))) or 0
+    eight, nine = _Stream(8), _Stream(9)
+    for s in (None, eight, eight, nine):
+        if s is None:
+            call.run()
+        elif given:
+            call.run(stream=s)
+        else:
+            with using(s):
+                call.run()
+    assert launched == [(7, []), (8, [8]), (8, [8]), (9, [8, 9])]
+    assert eight.waited == nine.waited == ["made"]
+    capturing.append(10)
+    ten = _Stream(10)
+    call.run(stream=ten)
+    assert t.streams[-1] == 10 and ten.waited == [] and launched[-1][0] == 10
+
+
 def test_ctypes_struct_matches_the_header(tmp_path):
     gcc = shutil.which("gcc") or shutil.which("cc")
     if gcc is None:
