@@ -103,13 +103,13 @@ template <int D>
 struct GqaSource {
   static constexpr int kPer = D / 32;             // lanes per row
   const GqaArgs& a;
-  int32_t seq, last, head, lane;
+  int32_t seq, head, lane;
   int32_t step = -1, ahead = -1;                  // first row of the step at hand; of the one looked up
   int32_t page[4];
   const uint8_t* at[4];                           // this lane's parts of row 0 of the step
-  bool ok = false;
-  __device__ __forceinline__ GqaSource(const GqaArgs& args, int32_t sq, int32_t p, int32_t h, int l)
-      : a(args), seq(sq), last(p), head(h), lane(l) {}
+  int32_t have = 0;                               // rows of the step that are there
+  __device__ __forceinline__ GqaSource(const GqaArgs& args, int32_t sq, int32_t h, int l)
+      : a(args), seq(sq), head(h), lane(l) {}
   __device__ __forceinline__ void look_up(int32_t p) {
     ahead = p;
     page[0] = load_page(a.map[0], a.page_shift[0], seq, p);
@@ -117,20 +117,19 @@ struct GqaSource {
 #pragma unroll
       for (int i = 1; i < 4; ++i) page[i] = load_page(a.map[i], a.page_shift[i], seq, p);
   }
-  // Moves to the step at row p; `then` (or -1) is the one after it.
-  __device__ __forceinline__ void go(int32_t p, int32_t then) {
+  // Moves to the step at row p, whose rows w sees; `then` (or -1) is the one after it.
+  __device__ __forceinline__ void go(int32_t p, const Seen& w, int32_t then) {
     if (ahead != p) look_up(p);
     step = p;
     int64_t r = 0;
-    ok = true;
+    have = kPageStep;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (i == 0 || !a.one_map) r = step_base(a.map[i], a.page_shift[i], seq, p, page[i], last);
-      ok = ok && r >= 0;
+      if (i == 0 || !a.one_map) r = step_rows(a.map[i], a.page_shift[i], seq, p, page[i], have);
       at[i] = a.base[i] + (r + (i & 1 ? lane : lane / kPer)) * a.rb[i] +
               (i & 1 ? head * (D / 32) : head * (D / 2) + (lane % kPer) * 16);
     }
-    if (!ok && lane == 0) record_error(a.status, CSA2_ERR_INDEX_RANGE);
+    if (have < kPageStep && lane == 0 && w.some(have, kPageStep - 1)) record_error(a.status, CSA2_ERR_INDEX_RANGE);
     if (then >= 0) look_up(then);
   }
   __device__ __forceinline__ uint32_t scales(int i, uint32_t off) const {
@@ -464,10 +463,15 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
       uint8_t* ring_s = gqa_s + warp * GqaRing<D>::warp;
       const uint32_t ring = smem_u32(ring_s);
       const Seen seen = seen_rows(pos, a.window, a.n_sink);
-      GqaSource<D> src(a, seq, pos, head, lane);
+      GqaSource<D> src(a, seq, head, lane);
       int32_t load = c0 + sub;
-      uint32_t ks = 0, vs = 0, bad = 0;            // scales on their way; stages whose rows are not there
+      uint32_t ks = 0, vs = 0, rooms = 0;          // scales on their way; rows that are there, a byte per stage
       int ls = 0, ws = 0;
+      auto rows_of = [&](int32_t p0, int32_t room) {   // what is seen of a tile's rows that are there
+        Seen w = seen.from(p0);
+        w.hi = min(w.hi, room - 1);
+        return w;
+      };
       auto start = [&]() {                         // starts the next tile's copies; its scales come back
         if (load < c1) {
           const int32_t p0 = ur.row(load, kRows), step = p0 & ~(kPageStep - 1);
@@ -475,10 +479,11 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
           if (step != src.step) {
             // the step after it, by the last tile of this one's reach
             const int32_t ahead = load + (kPageStep / kRows - 1) / share * share;
-            src.go(step, ahead < c1 ? ur.row(ahead, kRows) & ~(kPageStep - 1) : -1);
+            src.go(step, seen.from(step), ahead < c1 ? ur.row(ahead, kRows) & ~(kPageStep - 1) : -1);
           }
-          bad = src.ok ? bad & ~(1u << ls) : bad | (1u << ls);
-          if (src.ok) src.copy(p0 - step, ring + ls * GqaRing<D>::stage, seen.from(p0), ks, vs);
+          const int32_t room = max(0, min(kRows, src.have - (p0 - step)));
+          rooms = (rooms & ~(0xFFu << (8 * ls))) | ((uint32_t)room << (8 * ls));
+          if (room > 0) src.copy(p0 - step, ring + ls * GqaRing<D>::stage, rows_of(p0, room), ks, vs);
         }
         copies_commit();
       };
@@ -498,8 +503,8 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
         if (!first) put_scales();
         start();
         if (x >= c0) {
-          if (!((bad >> ws) & 1u))
-            tile_step<D, NT>(st, ring_s + ws * GqaRing<D>::stage, qf, qs, seen.from(ur.row(x, kRows)), g, t);
+          if (const int32_t room = (rooms >> (8 * ws)) & 0xFF)
+            tile_step<D, NT>(st, ring_s + ws * GqaRing<D>::stage, qf, qs, rows_of(ur.row(x, kRows), room), g, t);
           ws = ws + 1 == kStages ? 0 : ws + 1;
         }
       }

@@ -83,6 +83,11 @@ __device__ __forceinline__ TileRange tile_range(int32_t pos, int32_t window, int
 struct Seen {
   int32_t hi, lo, sk;
   __device__ __forceinline__ bool row(int32_t r) const { return r <= hi && (r >= lo || r < sk); }
+  // whether any of rows a to b is seen
+  __device__ __forceinline__ bool some(int32_t a, int32_t b) const {
+    const int32_t e = min(b, hi);
+    return max(a, lo) <= e || a <= min(e, sk - 1);
+  }
   __device__ __forceinline__ bool all(int32_t n) const { return n - 1 <= hi && (lo <= 0 || n <= sk); }
   __device__ __forceinline__ Seen from(int32_t p0) const { return Seen{hi - p0, lo - p0, sk - p0}; }
 };
@@ -151,17 +156,22 @@ __device__ __forceinline__ int32_t load_page(const RowMap& m, int32_t shift, int
   const int32_t pg = page_of(m, shift, p);
   return seq < 0 || pg >= m.max_pages ? -1 : __ldg(m.page_table + (int64_t)seq * m.max_pages + pg);
 }
-// Physical row of position p (a multiple of kPageStep), of whose step the
-// rows up to position `last` are wanted; -1 when they are not all in the plane.
-__device__ __forceinline__ int64_t step_base(const RowMap& m, int32_t shift, int32_t seq, int32_t p, int32_t page,
-                                             int32_t last) {
-  const int32_t n = min(kPageStep - 1, last - p);
-  int64_t r;
-  if (m.page_table)
-    r = page < 0 ? -1 : (int64_t)page * m.page_rows + (p - page_of(m, shift, p) * m.page_rows);
-  else
-    r = seq < 0 || (m.seq_rows > 0 && p + n >= m.seq_rows) ? -1 : (int64_t)seq * m.seq_rows + p;
-  return r >= 0 && r + n < m.n_rows ? r : -1;
+// Physical row of position p, a multiple of kPageStep; `have` falls to the
+// number of rows of its step that the plane holds for the sequence (a page may
+// be missing, a last page or the last sequence's share cut short).
+__device__ __forceinline__ int64_t step_rows(const RowMap& m, int32_t shift, int32_t seq, int32_t p, int32_t page,
+                                             int32_t& have) {
+  int64_t r, room;
+  if (m.page_table) {
+    r = (int64_t)page * m.page_rows + (p - page_of(m, shift, p) * m.page_rows);
+    room = page < 0 ? 0 : m.n_rows - r;
+  } else {
+    r = (int64_t)seq * m.seq_rows + p;
+    room = seq < 0 ? 0 : m.n_rows - r;
+    if (m.seq_rows > 0) room = min(room, m.seq_rows - p);
+  }
+  have = room >= have ? have : room > 0 ? (int32_t)room : 0;
+  return r;
 }
 
 // a / b of two counts, most of which fit 32 bits (a 64-bit division is long).

@@ -53,8 +53,7 @@ constexpr int kBatch = 16;                       // tiles whose places are worke
 // Where a tile is: worked out kBatch tiles at a time, a lane per step of 64
 // rows (done by every filling warp for itself, it took longer than the softmax).
 struct alignas(16) Place {
-  Seen seen;                                     // its rows that any query of the run sees
-  int32_t flags;                                 // bit s: step s is there; bit 2 + s: it should be and is not; bit 4: all rows
+  int32_t end[2], lo, sk;                        // its rows that are there and may be seen: of step s those below end[s], from lo or below sk
   uint32_t r[2][4];                              // first physical row of each step in each plane
   int32_t row, pad[3];                           // its first row
 };
@@ -433,37 +432,33 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       const int s = lane & 1;
       const bool in = t < it.c1;
       Place* pl = places + h * kBatch + (lane >> 1);
-      bool ok = false, bad = false;
-      int32_t p0 = 0;
+      bool bad = false;
+      int32_t p0 = 0, have = 0;
       Seen w{-1, 0, 0};
       if (in) {
-        const int32_t last = it.hi, seq = it.seq;
-        p0 = run_tiles(last, it.lo, a.n_sink).row(t, kT);
-        w = Seen{last, it.lo, a.n_sink}.from(p0);
+        const int32_t seq = it.seq;
+        p0 = run_tiles(it.hi, it.lo, a.n_sink).row(t, kT);
+        w = Seen{it.hi, it.lo, a.n_sink}.from(p0);
         // a step without a row to see may have no page
-        if (s * kPageStep <= w.hi && ((s + 1) * kPageStep > w.lo || s * kPageStep < w.sk)) {
-          const int32_t at = p0 + s * kPageStep;
+        const int32_t at = p0 + s * kPageStep;
+        const Seen ws = w.from(s * kPageStep);
+        if (ws.some(0, kPageStep - 1)) {
           uint32_t r0 = 0;
-          ok = true;
+          have = kPageStep;
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            if (y == 0 || !a.one_map) {
-              const int64_t b = step_base(a.map[y], a.page_shift[y], seq, at, load_page(a.map[y], a.page_shift[y], seq, at), last);
-              ok = ok && b >= 0;
-              r0 = (uint32_t)b;                  // rows of a plane fit 31 bits
-            }
+            if (y == 0 || !a.one_map)            // rows of a plane fit 31 bits
+              r0 = (uint32_t)step_rows(a.map[y], a.page_shift[y], seq, at, load_page(a.map[y], a.page_shift[y], seq, at), have);
             pl->r[s][y] = r0;
           }
-          bad = !ok;
+          bad = have < kPageStep && ws.some(have, kPageStep - 1);
         }
-      }
-      __syncwarp();
-      int32_t flags = (ok ? 1 << s : 0) | (bad ? 4 << s : 0);
-      flags |= __shfl_xor_sync(0xffffffffu, flags, 1);
-      if (in && s == 0) {
-        pl->seen = w;
-        pl->flags = flags | ((flags & 3) == 3 && w.all(kT) ? 16 : 0);
-        pl->row = p0;
+        pl->end[s] = s * kPageStep + min(have, w.hi + 1 - s * kPageStep);
+        if (s == 0) {
+          pl->lo = w.lo;
+          pl->sk = w.sk;
+          pl->row = p0;
+        }
       }
       if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(a.status, CSA2_ERR_INDEX_RANGE);
       __syncwarp();
@@ -594,8 +589,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       const uint8_t* const bks = a.base[1] + it.head * (D / 32);
       const uint8_t* const bv = a.base[2] + it.head * (D / 2) + blk32 * 16;
       const uint8_t* const bvs = a.base[3] + it.head * (D / 32);
-      Seen seen{-1, 0, 0};                       // the place of the tile whose loads are next
-      int32_t flags = 0;
+      int4 seen = {};                            // the place of the tile whose loads are next
       uint4 pr[2] = {};
       bool ok = true;
       auto rows_of = [&](int32_t x) {            // moves to tile x
@@ -605,9 +599,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
           ++batch;
         }
         const Place& pl = places[((batch - 1) & 1) * kBatch + j % kBatch];
-        const int4 w = *reinterpret_cast<const int4*>(&pl.seen);
-        seen = Seen{w.x, w.y, w.z};
-        flags = w.w;
+        seen = *reinterpret_cast<const int4*>(pl.end);
         pr[0] = *reinterpret_cast<const uint4*>(pl.r[0]);
         pr[1] = *reinterpret_cast<const uint4*>(pl.r[1]);
       };
@@ -633,7 +625,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
       auto has_k = [&](int j) { return j < EACH || fw < LEFT; };
       auto has_v = [&](int j) { return j < EACH || left < LEFT; };
       auto seen_row = [&](int rr) {              // whether row rr of the tile is to be read
-        return (flags & 16) || ((flags >> (rr >= kPageStep)) & 1 && seen.row(rr));
+        return rr < (rr >= kPageStep ? seen.y : seen.x) && (rr >= seen.z || rr < seen.w);
       };
       auto load_k = [&]() {
         ks = vs = 0;
@@ -781,13 +773,12 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         const int32_t j = x - it.c0;
         const Place& pl = places[((n_batch + j / kBatch) & 1) * kBatch + j % kBatch];
         const Seen w = live ? mine.from(pl.row) : Seen{kT, 0, 0};   // a row behind the last counts as seeing all
-        const int32_t bad0 = pl.flags & 4, bad1 = pl.flags & 8;
-        const bool full = __all_sync(0xffffffffu, w.all(kT) && !(bad0 | bad1));
-        // bits of columns [32 y, 32 y + 32) seen: c <= hi && (c >= lo || c < sk)
+        const int2 end = *reinterpret_cast<const int2*>(pl.end);
+        const bool full = __all_sync(0xffffffffu, w.all(kT) && end.x == kPageStep && end.y == kT);
+        // bits of columns [32 y, 32 y + 32) seen: c <= hi && (c >= lo || c < sk), of rows that are there
         auto below = [](int32_t k) { return k <= 0 ? 0u : (k >= 32 ? ~0u : (1u << k) - 1u); };
         auto see = [&](int y) {
-          if (y < 2 ? bad0 : bad1) return 0u;
-          return below(w.hi + 1 - 32 * y) & (~below(w.lo - 32 * y) | below(w.sk - 32 * y));
+          return below(min(w.hi + 1, y < 2 ? end.x : end.y) - 32 * y) & (~below(w.lo - 32 * y) | below(w.sk - 32 * y));
         };
         // The weights, 32 columns at a time, over the logits' columns.  The
         // reference moves only when a logit exceeds it by kLazy (past kFine in

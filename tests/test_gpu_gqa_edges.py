@@ -1,0 +1,98 @@
+"""Grouped-query attention where a cache ends: shares and pages that the buffer
+cuts short, and pages that were given back."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from kv_cache_decode_csa2_b200 import csa2 as B
+from tests.gqa_cases import DEV, PAGE, Cache, bf16, bounds
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+
+
+def attend(cache, q, seq, pos, window, n_sink, group):
+    """(out, lse, status word) of one call."""
+    out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full(q.shape[:2], 7.0, dtype=torch.float32, device=DEV)
+    call = B.GqaAttn(cache.c, q.to(DEV), torch.tensor(pos, dtype=torch.int32, device=DEV), out, window=window,
+                     n_sink=n_sink, seq_of_query=torch.tensor(seq, dtype=torch.int32, device=DEV), lse=lse,
+                     group_queries=group)
+    call.run()
+    return out.double().cpu().numpy(), lse.double().cpu().numpy(), int(call.status.item())
+
+
+def check(cache, q64, seq, pos, out, lse, window, n_sink, there):
+    """Every query against the oracle over the rows it sees of the first
+    there[sequence] positions."""
+    for i in range(len(pos)):
+        rows = O.visible_rows(int(pos[i]), window, n_sink)
+        rows = rows[rows < there[seq[i]]]
+        if len(rows) == 0:
+            assert (out[i] == 0).all() and (lse[i] == -np.inf).all(), f"query {i} sees nothing"
+            continue
+        o, l, spread, reach, total = O.gqa_attention(q64[i], cache.values("k", seq[i], rows),
+                                                     cache.values("v", seq[i], rows))
+        bo, bl = bounds(o, l, spread, reach, total, len(rows), cache.D)
+        assert (np.abs(out[i] - o) <= bo).all() and (np.abs(lse[i] - l) <= bl).all(), f"query {i} at {pos[i]}"
+
+
+WINDOWS = [(0, 0), (20, 3), (90, 2), (5, 0)]
+
+
+@pytest.mark.parametrize("window,n_sink", WINDOWS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group", [False, True])
+def test_a_last_share_cut_short(group, D, window, n_sink):
+    """Sequence 1's share of a contiguous plane ends after 100 of 128 rows:
+    a query past them is reported and sees those before, the others of its
+    run see theirs, and nothing is read behind the buffer."""
+    rng = np.random.default_rng(31)
+    cache = Cache(rng, 2, 128, 2, D, paged=False)
+    cache.c = B.KVCache(2, D, *(B.Rows(x[:228], seq_rows=128) for x in cache.dev.values()))
+    seq, pos = [1] * 6 + [0, 0], [99, 110, 64, 98, 127, 3, 127, 50]
+    q, q64 = bf16(1.5 * rng.standard_normal((8, 6, D)))
+    out, lse, status = attend(cache, q, seq, pos, window, n_sink, group)
+    assert status == 6
+    check(cache, q64, seq, pos, out, lse, window, n_sink, [128, 100])
+    good = [0, 2, 3, 5, 6, 7]
+    out, lse, status = attend(cache, q[good], [seq[i] for i in good], [pos[i] for i in good], window, n_sink, group)
+    assert status == 0
+    check(cache, q64[good], [seq[i] for i in good], [pos[i] for i in good], out, lse, window, n_sink, [128, 100])
+
+
+@pytest.mark.parametrize("window,n_sink", WINDOWS)
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (40, 2)])
+@pytest.mark.parametrize("group", [False, True])
+def test_a_last_page_cut_short(group, Hq, Hkv, window, n_sink):
+    """The plane ends 20 rows into the page that holds positions 64 to 127 of
+    sequence 0, in one plane after another; the pages behind it are whole."""
+    rng = np.random.default_rng(32)
+    D, last = 128, 5
+    for cut in range(4):
+        cache = Cache(rng, 2, 192, Hkv, D, paged=False)
+        table = np.array([[0, last, 2], [3, 1, 4]], np.int32)
+        rows = []
+        for i, x in enumerate(cache.planes.values()):
+            y = np.empty_like(x)
+            for s in range(2):
+                for p in range(3):
+                    y[table[s, p] * PAGE:(table[s, p] + 1) * PAGE] = x[s * 192 + p * PAGE:s * 192 + (p + 1) * PAGE]
+            d = torch.from_numpy(y).to(DEV)
+            rows.append(B.Rows(d[:last * PAGE + 20] if i == cut else d, page_table=torch.from_numpy(table).to(DEV)))
+        cache.c = B.KVCache(Hkv, D, *rows)
+        seq, pos = [0, 0, 0, 1, 1], [83, 70, 100, 191, 80]
+        q, q64 = bf16(1.5 * rng.standard_normal((5, Hq, D)))
+        out, lse, status = attend(cache, q, seq, pos, window, n_sink, group)
+        assert status == 6
+        check(cache, q64, seq, pos, out, lse, window, n_sink, [84, 192])
+        keep = [0, 1, 3, 4]
+        out, lse, status = attend(cache, q[keep], [seq[i] for i in keep], [pos[i] for i in keep], window, n_sink, group)
+        assert status == 0
+        check(cache, q64[keep], [seq[i] for i in keep], [pos[i] for i in keep], out, lse, window, n_sink, [84, 192])
