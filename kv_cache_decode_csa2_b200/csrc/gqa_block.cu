@@ -451,7 +451,10 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
               r0 = (uint32_t)step_rows(a.map[y], a.page_shift[y], seq, at, load_page(a.map[y], a.page_shift[y], seq, at), have);
             pl->r[s][y] = r0;
           }
-          bad = have < kPageStep && ws.some(have, kPageStep - 1);
+          // an error only if a query sees them: between the windows of far queries pages may have been given back
+          if (have < kPageStep && ws.some(have, kPageStep - 1))
+            for (int i = 0; i < it.n_q && !bad; ++i)
+              bad = seen_rows(position(a, it.q0 + i), a.window, a.n_sink).from(at).some(have, kPageStep - 1);
         }
         pl->end[s] = s * kPageStep + min(have, w.hi + 1 - s * kPageStep);
         if (s == 0) {

@@ -96,3 +96,31 @@ def test_a_last_page_cut_short(group, Hq, Hkv, window, n_sink):
         out, lse, status = attend(cache, q[keep], [seq[i] for i in keep], [pos[i] for i in keep], window, n_sink, group)
         assert status == 0
         check(cache, q64[keep], [seq[i] for i in keep], [pos[i] for i in keep], out, lse, window, n_sink, [84, 192])
+
+
+@pytest.mark.parametrize("group", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+def test_pages_given_back_between_far_windows(D, group):
+    """Queries of one run far apart: pages that no window or sink reaches are
+    gone from the table, in three ways; one that a window reaches is an error."""
+    rng = np.random.default_rng(33)
+    cache = Cache(rng, 1, 1024, 2, D, paged=True)
+    seq, pos = [0] * 5, [1000, 130, 131, 40, 1001]
+    q, q64 = bf16(1.5 * rng.standard_normal((5, 6, D)))
+    for window, n_sink, gone in ((20, 3, range(3, 15)), (2, 0, [1, *range(3, 15)]), (64, 70, range(4, 14))):
+        for value in (-1, -7, 10 ** 6):
+            table = cache.dev_table.clone()
+            table[0, list(gone)] = value
+            rows = [B.Rows(x, page_table=table) for x in cache.dev.values()]
+            call = B.KVCache(2, D, *rows)
+            was, cache.c = cache.c, call
+            out, lse, status = attend(cache, q, seq, pos, window, n_sink, group)
+            cache.c = was
+            assert status == 0
+            check(cache, q64, seq, pos, out, lse, window, n_sink, [1024])
+    table = cache.dev_table.clone()
+    table[0, 2] = -1
+    cache.c = B.KVCache(2, D, *(B.Rows(x, page_table=table) for x in cache.dev.values()))
+    out, lse, status = attend(cache, q, seq, pos, 20, 3, group)
+    assert status == 6
+    check(cache, q64[[0, 3, 4]], [0] * 3, [1000, 40, 1001], out[[0, 3, 4]], lse[[0, 3, 4]], 20, 3, [1024])
