@@ -743,7 +743,8 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
         }
         const int e = max((int)(top >> 7), 20);
         const float up = __uint_as_float((uint32_t)(268 - e) << 23);
-        qs = __uint_as_float((uint32_t)(e - 14) << 23) * a.scale_log2;
+        // (not 0, which would make the -inf of a row that is not seen a NaN)
+        qs = fmaxf(__uint_as_float((uint32_t)(e - 14) << 23) * a.scale_log2, 1e-38f);
         uint8_t* dst = sm + L::q + m * L::kPlane + r * 128;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {

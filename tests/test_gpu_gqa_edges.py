@@ -6,7 +6,7 @@ import torch
 
 import oracle as O
 from kv_cache_decode_csa2_b200 import csa2 as B
-from tests.gqa_cases import DEV, PAGE, Cache, bf16, bounds
+from tests.gqa_cases import DEV, PAGE, Cache, bf16, bounds, check_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +124,24 @@ def test_pages_given_back_between_far_windows(D, group):
     out, lse, status = attend(cache, q, seq, pos, 20, 3, group)
     assert status == 6
     check(cache, q64[[0, 3, 4]], [0] * 3, [1000, 40, 1001], out[[0, 3, 4]], lse[[0, 3, 4]], 20, 3, [1024])
+
+
+@pytest.mark.parametrize("group", [False, True])
+def test_logits_that_vanish(group):
+    """Zero and tiny queries under a tiny softmax scale: every row that is seen
+    weighs the same, none that is not."""
+    rng = np.random.default_rng(34)
+    cache = Cache(rng, 1, 200, 1, 128, paged=True)
+    q = rng.standard_normal((6, 4, 128))
+    q[0], q[2], q[3, 1], q[4] = 0, 0, 0, q[4] * 1e-30
+    q, q64 = bf16(q)
+    pos = [150, 151, 199, 30, 77, 0]
+    for window, n_sink in ((0, 0), (40, 3)):
+        out = torch.empty((6, 4, 128), dtype=torch.bfloat16, device=DEV)
+        lse = torch.empty((6, 4), device=DEV)
+        call = B.GqaAttn(cache.c, q.to(DEV), torch.tensor(pos, dtype=torch.int32, device=DEV), out, window=window,
+                         n_sink=n_sink, seq_of_query=torch.zeros(6, dtype=torch.int32, device=DEV), lse=lse,
+                         softmax_scale=1e-20, group_queries=group)
+        call.run()
+        B.check_status(call.status)
+        check_attention(cache, q64, [0] * 6, pos, out, lse, window, n_sink, scale=float(np.float32(1e-20)))
