@@ -145,3 +145,33 @@ def test_logits_that_vanish(group):
         call.run()
         B.check_status(call.status)
         check_attention(cache, q64, [0] * 6, pos, out, lse, window, n_sink, scale=float(np.float32(1e-20)))
+
+
+@pytest.mark.parametrize("D,G,nq", [(64, 40, 16384), (128, 40, 16384), (64, 300, 1400), (128, 1, 16384)])
+def test_more_blocks_than_threads(D, G, nq):
+    """The most queries of a call, in blocks of as few as one: the threads
+    that look for where a CTA starts have several blocks each."""
+    rng = np.random.default_rng(35)
+    lens = [900, 64, 333, 5, 128, 700, 1, 512]
+    cache = Cache(rng, 8, 900, 1, D, paged=True, lens=lens)
+    seq = np.repeat(np.arange(8), nq // 8)
+    pos = np.array([rng.integers(-1, lens[s]) for s in seq])
+    q, q64 = bf16(rng.standard_normal((nq, G, D)).astype(np.float32))
+    for window, n_sink in ((0, 0), (100, 3)):
+        out, lse, status = attend(cache, q, seq, pos, window, n_sink, True)
+        assert status == 0
+        check_attention(cache, q64, seq, pos, torch.from_numpy(out), torch.from_numpy(lse), window, n_sink,
+                        only=range(0, nq, nq // 60))
+
+
+@pytest.mark.parametrize("group", [False, True])
+@pytest.mark.parametrize("window,n_sink", [(1, 0), (7, 3), (64, 64), (128, 130), (129, 0), (300, 65), (2 ** 31 - 1, 5)])
+def test_windows_of_wide_heads(window, n_sink, group):
+    rng = np.random.default_rng(window % 1000 + n_sink)
+    cache = Cache(rng, 2, 700, 2, 128, paged=True)
+    pos = [0, 1, 2, 62, 63, 64, 65, 127, 128, 129, 191, 192, 300, 301, 302, 699]
+    seq = [0] * 8 + [1] * 8
+    q, q64 = bf16(1.5 * rng.standard_normal((16, 16, 128)))
+    out, lse, status = attend(cache, q, seq, pos, window, n_sink, group)
+    assert status == 0
+    check(cache, q64, seq, pos, out, lse, window, n_sink, [700, 700])
