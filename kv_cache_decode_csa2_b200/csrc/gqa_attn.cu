@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kGqaThreads, NT == 1 ? 2 : 1) gqa_split_kernel
   {
     const int per = (a.nq + kGqaThreads - 1) / kGqaThreads;
     const int i0 = min(tid * per, a.nq), i1 = min(i0 + per, a.nq);
-    const bool empty = looks_empty<kGqaThreads, int32_t>(a);
+    const bool empty = looks_empty<kGqaThreads>(a);
     int64_t n = 0;
     for (int i = i0; i < i1; ++i) n += tile_range<kRows>(position(a, i), a.window, a.n_sink).count;
     bool empties;

@@ -185,14 +185,11 @@ cudaError_t launch_gqa_combine(const GqaArgs& a, int32_t D, int32_t run_heads, i
 // The queries of a CTA: blockIdx.x, n_cta queries on, ...  Thread i looks at
 // the i-th: reports a position past every row and says whether one sees none.
 // (Read where the kernel starts; the answers meet at a barrier it has anyway.)
-// With a 64-bit index I the block kernel behind it comes out 2% faster (windowed
-// chunk of 4,096 queries 264 for 269 us), with 32 bits the split kernel's
-// start 0.7 us shorter (one query over 4,096 rows 12.9 for 13.6 us).
-template <int N, typename I>
+template <int N>
 __device__ __forceinline__ bool looks_empty(const GqaArgs& a) {
   bool empty = false;
-#pragma unroll(sizeof(I) == 4 ? 1 : 4)
-  for (I q = blockIdx.x + (I)a.n_cta * threadIdx.x; q < a.nq; q += (I)a.n_cta * N) {
+#pragma unroll 1
+  for (int32_t q = blockIdx.x + a.n_cta * threadIdx.x; q < a.nq; q += a.n_cta * N) {
     const int32_t p = __ldg(a.query_pos + q);
     if (p >= a.limit) record_error(a.status, CSA2_ERR_INDEX_RANGE);
     empty = empty || p < 0;

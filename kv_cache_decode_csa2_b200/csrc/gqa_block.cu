@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
   pdl_wait();      // launched while the grid before it drains
   pdl_trigger();
 
-  const bool empty = looks_empty<kBlockThreads, int64_t>(a);
+  const bool empty = looks_empty<kBlockThreads>(a);
 
   // ---- prologue: barriers, TMEM, and where this CTA's run of tiles starts
   if (tid == 0) {
