@@ -96,8 +96,9 @@ __device__ __forceinline__ Seen seen_rows(int32_t pos, int32_t window, int32_t n
 }
 
 // Weights are 2^(L - r): L the logit in log2 units, r the row's reference,
-// kOffset below the largest L so far (a whole number), until an L is more than
-// kLazy above that.
+// kOffset below the largest L so far, until an L is more than kLazy above that.
+// (The largest weight is then 2^kOffset, which f16 holds exactly: rows that one
+// weight dominates are half as far off as with a whole number for r.)
 //
 // While r is up to kFine, L - r is one fused multiply-add of a product of q and
 // k with its scale; an L rounded by itself is off by less than 2^-3 there.  Past
@@ -111,8 +112,7 @@ constexpr float kLazy = 5.f;
 constexpr float kOffset = 10.f;
 constexpr float kFine = 1 << 20, kExact = 1 << 24;
 __device__ __forceinline__ float reference(float largest) {       // -inf: no row yet
-  const float m = floorf(largest);
-  return fabsf(m) <= kExact ? m - kOffset : m;
+  return fabsf(largest) <= kExact ? largest - kOffset : largest;
 }
 __device__ __forceinline__ bool past_fine(float r) { return fabsf(r) > kFine && r != -INFINITY; }
 __device__ __forceinline__ float exponent(float s, float scale, float r) {

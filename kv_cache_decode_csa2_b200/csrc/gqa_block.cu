@@ -829,7 +829,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
           }
           // a whole number: weights already rounded are scaled exactly
           const bool done = past_fine(mo) && limit > -INFINITY;      // an earlier turn of this tile did what follows
-          float m_new = done ? mo : fmaxf(mo, reference(most + sub));
+          float m_new = done ? mo : fmaxf(mo, reference(floorf(most + sub)));
           const bool far = !done && (past_fine(mo) || past_fine(m_new));
           if (__any_sync(0xffffffffu, far)) {
             // these rows' logits, each rounded once, in the products' place, and the largest
@@ -848,7 +848,7 @@ __global__ void __launch_bounds__(kBlockThreads, 1) gqa_block_kernel(const __gri
               }
               tmem_st16(s_t + 16 * z, b);
             }
-            if (far) m_new = fmaxf(mo, reference(high));
+            if (far) m_new = fmaxf(mo, reference(floorf(high)));
           }
           const float f = mo == -INFINITY ? 0.f : ex2(mo - m_new);
           mo = m_new;
