@@ -418,18 +418,24 @@ int32_t csa2_kv_append_fp4_bf16(const uint16_t* q, const uint16_t* k, const uint
  *   query_pos    int32 [nq]; a query sees rows 0..query_pos[i]; a negative
  *                position sees none: its output is 0 and its lse -inf; one
  *                past the rows that a plane has for a sequence, or past 2^29 - 1,
- *                is CSA2_ERR_INDEX_RANGE and sees the rows before
+ *                is CSA2_ERR_INDEX_RANGE and sees the rows before.  So is a
+ *                row that a query sees and no page or plane holds: it counts as
+ *                not seen.  Pages whose rows no query of the call sees may be
+ *                missing (a negative entry, or one past the plane).
  *   softmax_scale  host; <= 0 means 1/sqrt(D)
  *   group_queries  nonzero: consecutive queries of one sequence share the rows
  *                they read (a prefill chunk, a speculative block); zero: every
  *                query reads alone (a decode batch).  The results are the same
- *                up to rounding, whatever the sequences and positions.
+ *                up to rounding, whatever the sequences and positions; the time
+ *                is that of all rows between the first and the last that any of
+ *                a sequence's neighbouring queries sees.
  *   out          bf16 [nq][Hq][D];  lse float [nq][Hq] or NULL, as
  *                csa2_sparse_attn_fp4 (parts combine with csa2_attn_combine)
- * Accumulation is fp32.  No value of a row that a query does not see reaches
- * its output, whatever bytes the row holds; of a row that it does see, a NaN
- * among the keys makes the head's output NaN, and one among the values at
- * least the output's values beside it (with group_queries all D).  Supported: D in {64, 128}; Hq a
+ * Accumulation is fp32; logits may be of any size that fp32 holds.  No value of
+ * a row that a query does not see reaches its output, whatever bytes the row
+ * holds; of a row that it does see, a NaN among the keys makes the head's output
+ * NaN, and one among the values at least the output's values beside it (with
+ * group_queries all D).  Supported: D in {64, 128}; Hq a
  * multiple of Hkv; 1 <= Hkv <= 256; Hq <= 1024; 1 <= nq <= 16384.
  */
 int32_t csa2_gqa_attn_fp4(const uint16_t* q, const csa2_kv_cache* cache, const int32_t* seq_of_query,
@@ -443,7 +449,10 @@ int32_t csa2_gqa_window_attn_fp4(const uint16_t* q, const csa2_kv_cache* cache, 
                                  const int32_t* query_pos, int32_t nq, int32_t Hq, int32_t window,
                                  int32_t n_sink, float softmax_scale, int32_t group_queries, uint16_t* out,
                                  float* lse, void* ws, size_t ws_bytes, int32_t* status, void* stream);
-/* Workspace of both calls (0: unsupported shape). */
+/* Workspace of both calls (0: unsupported shape): 22 MB at D = 64, 43 MB at
+ * D = 128, whatever the other sizes (256 rows of O for each of 320 parts of the
+ * work).  It needs no initialisation, and calls that run one after another may
+ * share one. */
 size_t csa2_gqa_attn_workspace(int32_t nq, int32_t Hq, int32_t Hkv, int32_t D);
 
 /* ------------------------------------------------------------ helpers */

@@ -20,10 +20,12 @@
 // of bf16's 8 bits for values down to 2^-28 of the row's largest.
 //
 // Measured on 64 query and 8 KV heads, D = 128: one query over 1,048,576 rows
-// 280 to 292 us (3.9 to 4.1 TB/s, 0.60 of the copy rate), 32 queries over
-// 572,000 rows 166 us (3.7 TB/s).  What bounds it is the expansion of the codes: the
-// conversions, byte permutes and f16 products issue at half rate and, with
-// the rest, fill 62% of the issue slots at four warps per scheduler.  Against
+// 281 to 308 us from GPU to GPU (3.7 to 4.1 TB/s, 0.57 to 0.62 of the copy
+// rate), 32 queries over 572,000 rows 167 to 176 us (3.5 to 3.7 TB/s); at D = 64,
+// 238 and 140 us.  No unit is full (ALU pipe 55%, issue slots 62%, DRAM 44%,
+// tensor pipe 21%): four warps per scheduler wait for their own instructions
+// before, for the half-rate pipe of conversions, permutes and f16 products and
+// for the issue slot, 1.6, 0.9 and 1.1 warps per issue.  Against
 // what stood when each was tried, 16-row tiles took 383 us for 326, V of a
 // tile beside K of the next 348 for 322, two chains of MMAs per logit tile 299
 // for 292, and 80 registers for a third CTA per SM 429 for 292 (spills).
@@ -70,7 +72,7 @@ constexpr int kStages = 3;
 static_assert(kRows == 32 && kStages == 3, "a lane per row of scales, written a turn before they are read");
 // Tiles a CTA takes at least: one each makes as many parts as there are tiles
 // to join.  A query over 4,096 rows took 19.1, 16.8, 17.3, 18.8, 21.2 us with
-// 1, 2, 3, 4, 6 (12.9 us by now).
+// 1, 2, 3, 4, 6 (13.0 to 13.5 us by now).
 constexpr int kMinRun = 2;
 template <int D>
 struct GqaRing {

@@ -24,10 +24,11 @@
 // into the runs of its queries' sequences, one item each per KV head.
 //
 // Measured on 64 query and 8 KV heads, D = 128: 2,048 queries over 16,384 rows
-// 1.08 to 1.12 ms (920 to 954 TFLOP/s, 0.57 of the dense f16 rate), a windowed
-// chunk of 4,096 (1,024 rows and 4 sinks) 264 us, 8 blocks of 5 queries over
-// 158,000 rows 173 us.  A 128-row tile takes 4,700 clocks: 3,000 of softmax,
-// the rest products and hand-over, the other height's between them.
+// 1.10 to 1.14 ms (903 to 940 TFLOP/s, 0.55 to 0.57 of the dense f16 rate), a
+// windowed chunk of 4,096 (1,024 rows and 4 sinks) 266 to 269 us, 8 blocks of 5
+// queries over 158,000 rows 161 to 165 us; the chunk of 2,048 at D = 64 0.95 ms.
+// A 128-row tile takes 4,700 clocks: 3,000 of softmax, the rest products and
+// hand-over, the other height's between them.
 //
 // Rows a query does not see are masked in S; a value row must also not reach
 // it through 0 x NaN, so a NaN scale in V is taken as 0 there and its row's

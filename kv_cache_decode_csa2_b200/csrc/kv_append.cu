@@ -18,11 +18,13 @@
 // and stores are coalesced, a block's maximum is two shuffles, and the rotation
 // partner of the half-split layout is one shuffle away; for queries, which are
 // most of the work, it has both sides of eight pairs.  A slot walks `per` heads of
-// its token with the angles in registers, kBatch heads' loads in flight.
+// its token with the angles in registers, kBatch heads' loads in flight (queries:
+// two heads' of bf16, one of fp32).
 //
-// Measured on 64 query and 8 KV heads, D = 128, bf16: 32,768 tokens 272 us
-// (1.38 GB, 5.07 TB/s, 0.77 of the copy rate), 2,048 tokens 23.8 us (3.66
-// TB/s), 32 tokens 6.9 us, which is the launch.  What is left waits for loads.
+// Measured on 64 query and 8 KV heads, D = 128, bf16: 32,768 tokens 271 to 275 us
+// (1.38 GB, 5.05 TB/s, 0.77 of the copy rate), 2,048 tokens 23.9 us (3.65
+// TB/s), 32 tokens 6.5 to 7.1 us, which is the launch; 32,768 tokens of fp32 402
+// us (5.10 TB/s), of D = 64 145 us (4.75 TB/s).  What is left waits for loads.
 #include "csa2_device.cuh"
 #include "fp4_device.cuh"
 #include "internal.h"
@@ -301,8 +303,9 @@ __device__ __forceinline__ void append_rows(const AppendArgs& a, uint32_t tokens
 template <int D, bool F32, bool PAIRS>
 __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const __grid_constant__ AppendArgs a) {
   pdl_wait();      // launched while the grid before it drains
-  // chunks of the same tokens are neighbours: their rows lie together, and the
-  // arithmetic of keys and values runs beside the queries' traffic
+  // The chunks of a group of blocks are neighbours.  A query lane holds twice as
+  // many values, so a query block covers twice as many tokens as one of keys or
+  // values, and the query blocks of the grid's second half find no token left.
   const uint32_t tokens = blockIdx.x / (uint32_t)a.chunks;
   const int chunk = (int)(blockIdx.x - tokens * (uint32_t)a.chunks);
   if (chunk < a.first[1]) append_queries<D, F32, PAIRS>(a, tokens, chunk);
@@ -364,7 +367,8 @@ cudaError_t launch_kv_append(const void* q, const void* k, const void* v, bool f
   // One head per slot while the launch cannot fill the device; when it can,
   // enough heads that a slot's own reading (row, page, angles) is the smaller
   // part of what it reads (2,048 tokens of 64 + 2 x 8 heads: 27.4 us with four
-  // heads per slot, 26.0 us with sixteen).
+  // heads per slot, 26.0 us with sixteen).  Lanes are counted as for keys and
+  // values, a query head's twice.
   const int lph = c.D / 8;
   const int64_t lanes = (int64_t)n * (Hq + 2 * c.Hkv) * lph, full = (int64_t)sm_count() * 2048;
   a.per = lanes <= full ? 1 : lanes <= 8 * full ? kBatch : 4 * kBatch;
